@@ -352,6 +352,10 @@ def _handles(s):
                                  low_freq_factor=1.0, high_freq_factor=4.0, original_max_position=8192)
         s["h"] = {x: rv.heads(s[x]) for x in ("q", "k", "q_out", "k_out")}
         return
+    if c["op"] == "write" and T > c["block"]:
+        # a row may go back by `block` positions only: a pass that appends more begins from the tail as it was
+        s["tails"] = torch.stack([s["k_tail"], s["v_tail"]])
+        s["k_tail"], s["v_tail"], s["tails_before"] = s["tails"][0], s["tails"][1], s["tails"].clone()
     s["cache"] = rv.KV8(B, c["Hkv"], c["hd"], c["max_seq"], c["block"],
                         rv.KV8_INT8 if c["fmt"] == "int8" else rv.KV8_E4M3, rv.BF16 if c["act"] == "bf16" else rv.F16,
                         *(s[x + "_" + y].data_ptr() for y in ("codes", "scale", "tail") for x in "kv"))
@@ -369,6 +373,8 @@ def _run_own(s):
         return {"q": s["q_out"], "k": s["k_out"]}
     count = s["count"].data_ptr()
     if c["op"] == "write":
+        if "tails" in s:
+            s["tails"].copy_(s["tails_before"])
         rv.kv8_append(s["cache"], h["k"], h["v"], B, T, pos, count, None, stream)
         rv.kv8_read(s["cache"], h["k_out"], h["v_out"], B, s["longest"], s["first"].data_ptr(), s["span"].data_ptr(), None,
                     stream)
