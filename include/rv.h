@@ -266,6 +266,178 @@ int rv_greedy_head_noalloc(const void *d_lm_head, const void *d_final_norm, cons
  * counts only the resident backbone. */
 int rv_offload_backbone(rv_model *m, int keep_layers);
 
+/* ------------------------------------------------------------ operators
+ * Stand-alone operators of long-context serving, on device memory that the
+ * caller owns: rotary positions, an 8-bit K/V cache (written, read back) and
+ * the attention that reads it.  The 8-bit model cache (RV_OPT_KV_CACHE) runs
+ * the same kernels.  The pages have no counterpart: they leave the cache in
+ * 16 bits and the positions unscaled; long contexts are where both cost
+ * (paperlayer.ai section 5, "Memory Efficiency").
+ *
+ * Every pointer in these calls is a DEVICE pointer of the current device
+ * unless it names a struct; the calls are asynchronous on `stream` (a
+ * cudaStream_t of that device, NULL = default stream), allocate nothing,
+ * keep nothing between calls and may be captured into a graph.  A captured
+ * call holds the pointers and the struct values it was given; positions and
+ * counts are read when it runs.  All arguments are checked on the host
+ * before any launch (RV_EINVAL); positions and counts, which live on the
+ * device, are checked there as each call says.
+ *
+ * A batch has B rows of up to T tokens.  d_pos[b] is the position of row b's
+ * first token (NULL: 0), token t sits at d_pos[b] + t, and d_count[b] says
+ * how many of the T tokens row b has (NULL: T for every row; values outside
+ * 0..T are taken as the nearer end).  Tokens at or beyond the count are
+ * neither read nor written: what their output rows held stays. */
+#define RV_F16 0
+#define RV_BF16 1
+#define RV_F32 2
+
+/* A tensor [B][T][heads][head_dim] of heads.  The head dimension is
+ * contiguous; the strides are in elements, rows start on 16-byte boundaries
+ * (data and every stride that is used), and an output's rows must not
+ * overlap.  An output may be the input itself (same data and strides) where
+ * a call says "in place"; any other overlap of the two is the caller's
+ * mistake and not detected. */
+typedef struct rv_heads {
+  void *data;
+  int dtype; /* RV_F16, RV_BF16 or RV_F32 */
+  int heads;
+  int64_t stride_b, stride_t, stride_h;
+} rv_heads;
+
+/* Rotary positions: element pair i of a head's first rotary_dim elements is
+ * turned by the angle p * f(i) at position p and scaled by the attention
+ * factor; the rest of the head is copied.  Pairs are (i, i + rotary_dim/2)
+ * in the half layout and (2i, 2i + 1) in the interleaved one.  With
+ * f0(i) = theta^(-2i/rotary_dim), frequencies for contexts longer than the
+ * ones trained on:
+ *   RV_ROPE_PLAIN   f = f0
+ *   RV_ROPE_LINEAR  f = f0 / factor
+ *   RV_ROPE_BASE    f0 with theta * factor^(r/(r-2)), r = rotary_dim (the
+ *                   fastest pair keeps its frequency, the slowest is
+ *                   divided by factor); rotary_dim > 2
+ *   RV_ROPE_BANDS   f = k f0 + (1-k) f0/factor, k = clamp((original_max_position
+ *                   f0/2pi - low_freq_factor) / (high_freq_factor -
+ *                   low_freq_factor), 0, 1)
+ *   RV_ROPE_RAMP    f = (1-u) f0 + u f0/factor, u = clamp((i - lo)/(hi - lo),
+ *                   0, 1), lo = floor(c(beta_fast)) and hi = ceil(c(beta_slow))
+ *                   clamped to [0, r-1] (hi = lo + 0.001 where they meet),
+ *                   c(n) = r ln(original_max_position/(2 pi n))/(2 ln theta);
+ *                   attention_factor 0 means 0.1 ln(factor) + 1 (1 if
+ *                   factor <= 1) */
+#define RV_ROPE_HALF 0
+#define RV_ROPE_INTERLEAVED 1
+#define RV_ROPE_PLAIN 0
+#define RV_ROPE_LINEAR 1
+#define RV_ROPE_BASE 2
+#define RV_ROPE_BANDS 3
+#define RV_ROPE_RAMP 4
+typedef struct rv_rope_config {
+  int head_dim, rotary_dim; /* multiples of 16, rotary_dim <= head_dim <= 256 */
+  int layout, scaling;
+  int original_max_position; /* BANDS, RAMP: > 0 */
+  double theta;              /* > 1 */
+  double factor;             /* > 0; every scaling but PLAIN */
+  double low_freq_factor, high_freq_factor; /* BANDS: 0 < low < high */
+  double beta_fast, beta_slow;              /* RAMP: fast > slow > 0 */
+  double attention_factor; /* factor on the rotated part; 0: 1 (RAMP: see above) */
+} rv_rope_config;
+
+/* What rv_rope needs of a configuration, filled in by rv_rope_init (host
+ * arithmetic, no device work) and kept by the caller.  turns[i] is pair i's
+ * frequency in turns per position as a 64-bit binary fraction: position x
+ * turns wraps exactly at whole turns, so far positions lose no precision. */
+typedef struct rv_rope_plan {
+  int head_dim, rotary_dim, layout;
+  float attention_factor;
+  uint64_t turns[128];
+} rv_rope_plan;
+
+int rv_rope_init(const rv_rope_config *cfg, rv_rope_plan *plan);
+
+/* Rotate B x T tokens' query heads and key heads (k_in and k_out both NULL:
+ * queries alone) in one launch.  q_in/q_out and k_in/k_out have the same
+ * number of heads; in and out may be in place.  All four share one dtype, or
+ * the inputs are RV_F32 and the outputs one 16-bit type.  inverse != 0 turns
+ * the other way (and scales by the same attention factor): that is the
+ * gradient of the rotation, dL/dx from dL/dy.  The arithmetic is fp32, each
+ * output rounded once.  Any int32 position, negative ones included. */
+int rv_rope(const rv_rope_plan *plan, const rv_heads *q_in, const rv_heads *q_out, const rv_heads *k_in,
+            const rv_heads *k_out, int B, int T, const int32_t *d_pos, const int32_t *d_count, int inverse,
+            void *stream);
+
+/* An 8-bit K/V cache of one layer, in memory the caller owns.  A block is
+ * `block` consecutive positions of one row and one KV head; its K values
+ * share one scale and its V values another:
+ *   s = max(up8(amax / Q), 2^-100),  Q = 127 (RV_KV8_INT8), 448 (RV_KV8_E4M3),
+ * amax the largest magnitude among the block's present values and up8 the
+ * next number of 8 significant bits (so that x / s has no near ties: every
+ * rounding is the exact one).  A code is x / s rounded to the nearest code,
+ * ties to even, and stands for code * s.  A block with a NaN or an infinity
+ * among its values has a NaN scale: it reads back as NaN, and so does the
+ * attention of every query row that sees a position of it.
+ * The scales are a function of the values alone, however they were appended:
+ * the last 2 x block originals of each row and KV head stay in 16 bits in
+ * the tail (slot = position mod 2 block), and an append that ends in an open
+ * block quantises the block anew from originals.
+ * Layouts, all contiguous, N = max_seq rounded up to a multiple of block:
+ *   codes [max_batch][n_kv_heads][N][head_dim], one byte each
+ *   scale [max_batch][n_kv_heads][N / block], fp32
+ *   tail  [max_batch][n_kv_heads][2 block][head_dim], act_dtype
+ * 16-byte aligned.  No initial contents are needed. */
+#define RV_KV8_INT8 0
+#define RV_KV8_E4M3 1
+typedef struct rv_kv8 {
+  int max_batch, n_kv_heads, head_dim, max_seq; /* head_dim 64 or 128 */
+  int block;     /* 16, 32, 64 or 128 */
+  int format;    /* RV_KV8_* */
+  int act_dtype; /* RV_F16 or RV_BF16: the type of the originals */
+  void *k_codes, *v_codes;
+  float *k_scale, *v_scale;
+  void *k_tail, *v_tail;
+} rv_kv8;
+
+/* Append B x T tokens' K and V (n_kv_heads heads each; act_dtype, or RV_F32
+ * rounded to act_dtype first) at positions d_pos[b].. of rows 0..B-1.  The
+ * positions before d_pos[b] must have been appended before.  A row may go
+ * back (drafted tokens refused) by at most `block` positions below the
+ * highest one written since, and continue from there; what lay behind is
+ * forgotten.  Rows of count 0 are left alone.  A row whose d_pos is negative
+ * or at least max_seq is left alone, and tokens at max_seq and beyond are
+ * dropped: either sets bit 6 (64) of *d_err (or NULL: not reported). */
+int rv_kv8_append(const rv_kv8 *cache, const rv_heads *k, const rv_heads *v, int B, int T, const int32_t *d_pos,
+                  const int32_t *d_count, int32_t *d_err, void *stream);
+
+/* Read positions d_pos[b] .. d_pos[b] + count - 1 of rows 0..B-1 back into
+ * k_out and v_out (either may be NULL): code * scale, exact in RV_F32, else
+ * rounded to RV_F16 / RV_BF16 with the type's largest finite value as the
+ * limit.  The positions must have been appended.  Positions outside
+ * 0..max_seq-1 leave their output rows alone and set bit 6 of *d_err. */
+int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_out, int B, int T, const int32_t *d_pos,
+                const int32_t *d_count, int32_t *d_err, void *stream);
+
+/* Attention of T new tokens per row (1..16: decoding, or drafted tokens to
+ * verify) over the cache.  Query token t of row b sees positions
+ * 0 .. d_pos[b] + t (its own included: append first), at most max_seq of
+ * them; out = softmax(scale * q k^T) v with query head h on KV head
+ * h / (heads / n_kv_heads).  A token that sees nothing (d_pos[b] + t < 0)
+ * gives zeros.  q is act_dtype (RV_F32: rounded to it first); out is
+ * act_dtype or RV_F32.  d_lse (NULL or fp32 [B][T][heads], contiguous)
+ * receives the natural log of the softmax denominators (-infinity where
+ * nothing is seen), with which partial results over several caches can be
+ * merged.  Scores, softmax and sums are fp32; the probabilities enter the
+ * product with V as fp16.  workspace: rv_kv8_attention_workspace bytes,
+ * 16-byte aligned, no contents needed or kept; calls that may run at the
+ * same time (other streams, graphs replayed concurrently) need one each. */
+int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, float scale,
+                     const int32_t *d_pos, const int32_t *d_count, float *d_lse, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of rv_kv8_attention for up to B rows, T tokens and n_heads
+ * query heads on the current device; 0 with rv_last_error() set if the
+ * arguments are bad.  Enough for every smaller B and T. */
+size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads);
+
 /* Sizes, for callers that allocate dump buffers.  rv_param_bytes: which = 0,
  * the 16-bit parameters resident on the device (embedding, LM head, norms,
  * backbone layers 1..keep_layers); which = 1, the river (codes and

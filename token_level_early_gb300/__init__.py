@@ -20,7 +20,8 @@ _ROOT = os.path.dirname(_HERE)
 LIB_PATH = os.path.join(_HERE, "librv.so")
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_ROOT, "_build")
-SOURCES = ["api.cu", "decode_b1.cu", "attention.cu", "general.cu", "quant.cu", "noalloc.cu", "stream.cu", "gemm_tc.cu", "rows_mma.cu"]
+SOURCES = ["api.cu", "decode_b1.cu", "attention.cu", "general.cu", "quant.cu", "noalloc.cu", "stream.cu", "gemm_tc.cu", "rows_mma.cu",
+           "rope.cu", "kv8.cu", "kv8_attention.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 RV_OK, RV_EINVAL, RV_ENOMEM, RV_ECUDA, RV_ECAPACITY, RV_ESTATE, RV_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
@@ -29,10 +30,15 @@ DUMP_HIDDEN, DUMP_S, DUMP_LOGITS, DUMP_KV, DUMP_LENS = range(5)
 EXPORTED = ("rv_last_error", "rv_load_model", "rv_quantize_river", "rv_export_river", "rv_prefill",
             "rv_decode_step", "rv_decode_step_dev", "rv_sync_status", "rv_kv_reset", "rv_set_debug",
             "rv_debug_dump", "rv_kv_bytes", "rv_param_bytes", "rv_free_model", "rv_time_kernel", "rv_greedy_head_noalloc", "rv_offload_backbone",
-            "rv_set_option", "rv_debug_fail_alloc", "rv_decode_attention_plan")
+            "rv_set_option", "rv_debug_fail_alloc", "rv_decode_attention_plan",
+            "rv_rope_init", "rv_rope", "rv_kv8_append", "rv_kv8_read", "rv_kv8_attention", "rv_kv8_attention_workspace")
 OPT_DECODE_ENGINE, ENGINE_CHAIN, ENGINE_PERSISTENT = 0, 0, 1
 OPT_QUANTIZER, QUANT_RTN, QUANT_HQQ = 1, 0, 1
 OPT_WAIT_LIMIT_US = 2
+F16, BF16, F32 = 0, 1, 2
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP = range(5)
+KV8_INT8, KV8_E4M3 = 0, 1
 TIME_GATEUP, TIME_O, TIME_LMHEAD, TIME_ATTN = 0, 1, 2, 3
 
 
@@ -85,6 +91,36 @@ class RVConfig(ctypes.Structure):
                 ("max_batch", ctypes.c_int), ("max_seq", ctypes.c_int)]
 
 
+class Heads(ctypes.Structure):
+    """rv_heads: a device tensor [B][T][heads][head_dim] (strides in elements); see also heads()."""
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int), ("heads", ctypes.c_int),
+                ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64), ("stride_h", ctypes.c_int64)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("scaling", ctypes.c_int), ("original_max_position", ctypes.c_int), ("theta", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("attention_factor", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    """rv_rope_plan, as rope_plan() fills it in."""
+    _fields_ = [("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int), ("layout", ctypes.c_int),
+                ("attention_factor", ctypes.c_float), ("turns", ctypes.c_uint64 * 128)]
+
+
+class KV8(ctypes.Structure):
+    """rv_kv8: an 8-bit K/V cache of one layer in the caller's device memory
+    (k_codes .. v_tail are device pointers; layouts in include/rv.h)."""
+    _fields_ = [("max_batch", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("max_seq", ctypes.c_int), ("block", ctypes.c_int), ("format", ctypes.c_int),
+                ("act_dtype", ctypes.c_int), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("k_tail", ctypes.c_void_p),
+                ("v_tail", ctypes.c_void_p)]
+
+
 class RVError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"rv error {code}: {msg}")
@@ -126,6 +162,15 @@ def lib():
         "rv_debug_fail_alloc": ([i32], i32),
         "rv_decode_attention_plan": ([i32, i32, i32, i32, i32, i32, ctypes.POINTER(i32)], i32),
     }
+    hp, kp, rp = ctypes.POINTER(Heads), ctypes.POINTER(KV8), ctypes.POINTER(RopePlan)
+    sig.update({
+        "rv_rope_init": ([ctypes.POINTER(RopeConfig), rp], i32),
+        "rv_rope": ([rp, hp, hp, hp, hp, i32, i32, vp, vp, i32, vp], i32),
+        "rv_kv8_append": ([kp, hp, hp, i32, i32, vp, vp, vp, vp], i32),
+        "rv_kv8_read": ([kp, hp, hp, i32, i32, vp, vp, vp, vp], i32),
+        "rv_kv8_attention": ([kp, hp, hp, i32, i32, f32, vp, vp, vp, vp, sz, vp], i32),
+        "rv_kv8_attention_workspace": ([kp, i32, i32, i32], sz),
+    })
     for name, (args, res) in sig.items():
         f = getattr(L, name)
         f.argtypes = args
@@ -165,6 +210,66 @@ def debug_fail_alloc(after: int) -> None:
     """Test hook: the device allocation after the next `after` ones fails
     (once); after < 0 turns it off (rv_debug_fail_alloc)."""
     _check(lib().rv_debug_fail_alloc(int(after)))
+
+
+_DTYPES = {"torch.float16": F16, "torch.bfloat16": BF16, "torch.float32": F32}
+
+
+def heads(tensor) -> Heads:
+    """Heads of a torch CUDA tensor [B][T][heads][head_dim] (any strides with a
+    contiguous last dimension); the tensor must outlive the calls that use it."""
+    if tensor.dim() != 4 or (tensor.shape[-1] > 1 and tensor.stride(-1) != 1):
+        raise ValueError("a [B][T][heads][head_dim] tensor with a contiguous last dimension is needed")
+    if str(tensor.dtype) not in _DTYPES:
+        raise ValueError(f"unsupported dtype {tensor.dtype}")
+    sb, st, sh, _ = tensor.stride()
+    return Heads(tensor.data_ptr(), _DTYPES[str(tensor.dtype)], tensor.shape[2], sb, st, sh)
+
+
+def rope_plan(head_dim: int, rotary_dim: Optional[int] = None, layout: int = ROPE_HALF, theta: float = 10000.0,
+              scaling: int = ROPE_PLAIN, factor: float = 1.0, low_freq_factor: float = 1.0,
+              high_freq_factor: float = 4.0, original_max_position: int = 0, beta_fast: float = 32.0,
+              beta_slow: float = 1.0, attention_factor: float = 0.0) -> RopePlan:
+    """rv_rope_init: the plan of a rotary configuration (host arithmetic, no GPU needed)."""
+    cfg = RopeConfig(head_dim, head_dim if rotary_dim is None else rotary_dim, layout, scaling, original_max_position,
+                     theta, factor, low_freq_factor, high_freq_factor, beta_fast, beta_slow, attention_factor)
+    plan = RopePlan()
+    _check(lib().rv_rope_init(ctypes.byref(cfg), ctypes.byref(plan)))
+    return plan
+
+
+def rope(plan: RopePlan, q_in: Heads, q_out: Heads, k_in: Optional[Heads], k_out: Optional[Heads], B: int, T: int,
+         d_pos: Optional[int], d_count: Optional[int] = None, inverse: bool = False, stream: Optional[int] = None):
+    """rv_rope: rotate query and key heads (inverse: the gradient's direction)."""
+    _check(lib().rv_rope(plan, q_in, q_out, k_in, k_out, B, T, d_pos, d_count, inverse, stream))
+
+
+def kv8_append(cache: KV8, k: Heads, v: Heads, B: int, T: int, d_pos: Optional[int], d_count: Optional[int] = None,
+               d_err: Optional[int] = None, stream: Optional[int] = None):
+    """rv_kv8_append: quantise new K/V into the cache."""
+    _check(lib().rv_kv8_append(cache, k, v, B, T, d_pos, d_count, d_err, stream))
+
+
+def kv8_read(cache: KV8, k_out: Optional[Heads], v_out: Optional[Heads], B: int, T: int, d_pos: Optional[int],
+             d_count: Optional[int] = None, d_err: Optional[int] = None, stream: Optional[int] = None):
+    """rv_kv8_read: read positions of the cache back as values."""
+    _check(lib().rv_kv8_read(cache, k_out, v_out, B, T, d_pos, d_count, d_err, stream))
+
+
+def kv8_attention_workspace(cache: KV8, B: int, T: int, n_heads: int) -> int:
+    """rv_kv8_attention_workspace: bytes of workspace for kv8_attention."""
+    n = lib().rv_kv8_attention_workspace(cache, B, T, n_heads)
+    if n == 0 and lib().rv_last_error():
+        raise RVError(RV_EINVAL, lib().rv_last_error().decode(errors="replace"))
+    return int(n)
+
+
+def kv8_attention(cache: KV8, q: Heads, out: Heads, B: int, T: int, scale: float, d_pos: Optional[int],
+                  d_count: Optional[int], d_lse: Optional[int], workspace: Optional[int], workspace_bytes: int,
+                  stream: Optional[int] = None):
+    """rv_kv8_attention: attention of T new tokens per row over the cache."""
+    _check(lib().rv_kv8_attention(cache, q, out, B, T, scale, d_pos, d_count, d_lse, workspace, workspace_bytes,
+                                  stream))
 
 
 def config_of(shape, max_batch: int, max_seq: int) -> RVConfig:

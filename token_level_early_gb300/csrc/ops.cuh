@@ -1,0 +1,91 @@
+// Shared pieces of the stand-alone operators (rope.cu, kv8.cu, kv8_attention.cu):
+// tensor descriptors as the kernels see them, host checks, and the internal
+// launchers that the model's own paths call.
+#pragma once
+
+#include <stddef.h>
+
+#include "../../include/rv.h"
+#include "common.cuh"
+#include "kernels.cuh"
+
+namespace rv {
+
+// Records the message and returns the code.
+int op_fail(int code, const char *fmt, ...);
+
+// A [B][T][heads][head_dim] tensor (strides in elements).
+struct Heads {
+  void *p;
+  int64_t sb, st, sh;
+};
+inline Heads heads_of(const rv_heads *h) { return h ? Heads{h->data, h->stride_b, h->stride_t, h->stride_h} : Heads{}; }
+
+// Unsigned division by a run-time constant: q = (x * m) >> 32 with m =
+// floor(2^32 / d) + 1 is exact for x * d < 2^32 (the error x / 2^32 * (m d -
+// 2^32) / d stays below 1 / d).
+struct FastDiv {
+  uint32_t d, m;
+};
+inline FastDiv fast_div(uint32_t d) { return FastDiv{d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
+__device__ __forceinline__ uint32_t div_by(uint32_t x, FastDiv f) { return f.d == 1 ? x : __umulhi(x, f.m); }
+
+// A row's token count and first position (see the conventions in rv.h).
+__device__ __forceinline__ int row_count(const int32_t *count, int b, int T) {
+  return count ? min(max(__ldg(count + b), 0), T) : T;
+}
+__device__ __forceinline__ int row_pos(const int32_t *pos, int b) { return pos ? __ldg(pos + b) : 0; }
+
+constexpr int kKv8ErrPos = 64;  // bit 6 of *d_err: a position outside the cache
+
+// Checks one tensor: pointer, dtype, head count, 16-byte rows; for outputs,
+// that no two rows overlap.  Returns RV_OK or RV_EINVAL with the message set.
+int check_heads(const char *what, const rv_heads *h, int B, int T, int head_dim, bool output);
+int check_batch(int B, int T);
+// RV_EINVAL if p is not device (or managed) memory of the current device.
+int check_device(const char *what, const void *p);
+
+// Rotary positions.
+struct RopeArgs {
+  Heads in[2], out[2];  // q, k
+  int H[2];
+  int B, T;
+  const int32_t *pos, *count;
+  int inverse;
+};
+cudaError_t launch_rope(const rv_rope_plan &plan, const RopeArgs &a, int in_dtype, int out_dtype, cudaStream_t s);
+// (cos, sin) of positions 0..T-1 x head_dim/2 pairs, times the attention factor.
+cudaError_t launch_rope_table(const rv_rope_plan &plan, float2 *cs, int T, cudaStream_t s);
+
+// 8-bit K/V cache.
+struct Kv8 {
+  uint8_t *codes[2];
+  float *scale[2];
+  uint16_t *tail[2];
+  int B, Hkv, hd, T, N, block, fmt, act;  // T = max_seq, N = T rounded up to a block
+};
+Kv8 kv8_of(const rv_kv8 *c);
+struct Kv8Io {
+  Heads k, v;
+  int B, T;
+  const int32_t *pos, *count;
+  int32_t *err;
+};
+cudaError_t launch_kv8_append(const Kv8 &c, const Kv8Io &io, int in_dtype, cudaStream_t s, int pdl = 0);
+cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaStream_t s);
+
+struct Kv8AttnArgs {
+  Kv8 c;
+  Heads q, out;
+  int H, B, T;
+  int q_f32, out_dtype;
+  int round_out;  // RV_F32 output rounded to act_dtype (the model's activations)
+  float scale;
+  const int32_t *pos, *count;
+  float *lse;
+  void *work;
+};
+size_t kv8_attention_work(const Kv8 &c, int B, int T, int H, int n_sm);
+cudaError_t launch_kv8_attention(const Kv8AttnArgs &a, int n_sm, cudaStream_t s, int pdl = 0);
+
+}  // namespace rv
