@@ -45,39 +45,50 @@ def quantise(x, fmt, block):
     return out, np.array(sc)
 
 
-def attention(q, k, v, scale, n):
-    """q [hd], k and v [N][hd], n visible -> (out, lse, A, D): A = sum of weights x |v|, D = the
-    largest scale x sum |q k| (what the rounding of a score is relative to)."""
-    hd = q.shape[-1]
-    if n <= 0:
-        return np.zeros(hd), -math.inf, np.zeros(hd), 0.0
-    k, v = k[:n], v[:n]
-    z = scale * (k @ q)
-    d = abs(scale) * float((np.abs(k) @ np.abs(q)).max())
-    m = z.max()
-    w = np.exp(z - m)
-    l = w.sum()
-    return (w @ v) / l, m + math.log(l), (w @ np.abs(v)) / l, d
-
-
-def attention_tolerance(ref, A, D, v, n, dtype):
-    """Error bound of one output row, by arithmetic:
-    - scores are fp32 sums of up to 128 products and two scalings: relative to
-      the sum of magnitudes at most (128 + 3) 2^-24 < 2^-16.9, so a weight is
-      off by a factor exp(2 x 2^-16.9 D) at most (score and maximum);
+def attention(q, k, v, scale, n, block):
+    """q [hd], k and v [N][hd], n visible -> (out, lse, bound): bound(dtype) is what the kernel's
+    output may be off by, from arithmetic:
+    - a score is a sum of up to 128 products, exact each, added to an fp32 sum
+      16 at a time, and two scalings: at most 2 x 8 + 4 roundings of 2^-24,
+      below 2^-19, relative to the sum of magnitudes.  int8 K codes enter as
+      code + 128 and -128 x sum q is taken off in the same sum, so the
+      magnitudes are those of 2 x the block's largest |k| for every element:
+      D = max scale x sum |q| x 2 ktop.  A weight is off by a factor exp(2 x
+      2^-19 D) at most (its score and the maximum);
     - a weight enters the product as fp16: half a step 2^-11 relative, or
       2^-25 absolute for weights below 2^-14 of the largest;
     - the exponential, the fp32 sums over at most a few thousand partial
-      products in order and the joins: below 2^-12 relative to A together;
+      products in order and the joins: below 2^-12 relative to A = sum of
+      weights x |v| together;
+    - int8 V codes enter the products as code + 128, and -128 x the sum of the
+      weights is taken off in the same fp32 sum: up to 6 roundings per tile of
+      sums below 256 x (sum of weights), each 2^-24 relative, is less than
+      2^-13.4 of a code step, and a step is the block's largest magnitude /
+      127: 2^-20 x sum of weights x (largest |v| of its block);
     - the output's own half step."""
-    vmax = np.abs(v[:max(n, 1)]).max(axis=0)
-    rel = 2.0 ** -11 + 2.0 ** -12 + 2.0 * 2.0 ** -16.9 * D
-    return rel * A + n * 2.0 ** -25 * vmax * 2.0 + U[dtype] * np.abs(ref) + 1e-30
+    hd = q.shape[-1]
+    if n <= 0:
+        return np.zeros(hd), -math.inf, 0.0, None
+    ktop, top = (np.array([np.abs(x[i:i + block]).max() for i in range(0, x.shape[0], block)]).repeat(block)[:n] for x in (k, v))
+    k, v = k[:n], v[:n]
+    z = scale * (k @ q)
+    d = abs(scale) * float((2.0 * ktop * np.abs(q).sum()).max())
+    m = z.max()
+    w = np.exp(z - m)
+    l = w.sum()
+    w /= l
+    out, A, S = w @ v, w @ np.abs(v), float(w @ top)
+    rel = 2.0 ** -11 + 2.0 ** -12 + 2.0 * 2.0 ** -19 * d
+
+    def bound(dtype):
+        return rel * A + 2.0 ** -20 * S + n * 2.0 ** -24 * np.abs(v).max(axis=0) + U[dtype] * np.abs(out) + 1e-30
+
+    return out, m + math.log(l), d, bound
 
 
 def lse_tolerance(lse, D):
     """fp32: the score's error, the sum's (below 2^-13 for up to a few thousand terms) and the result's steps."""
-    return 2.0 ** -16.9 * D + 2.0 ** -13 + 2.0 ** -22 * abs(lse)
+    return 2.0 ** -19 * D + 2.0 ** -13 + 2.0 ** -22 * abs(lse)
 
 
 def rope_frequencies(rotary_dim, theta, scaling="plain", factor=1.0, low=1.0, high=4.0, original=0, fast=32.0, slow=1.0):

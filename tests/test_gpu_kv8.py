@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import token_level_early_gb300 as rv
-from kv8_util import attention, attention_tolerance, lse_tolerance, quantise
+from kv8_util import attention, lse_tolerance, quantise
 
 pytestmark = pytest.mark.gpu
 
@@ -264,12 +264,12 @@ def check_attention(c, kk, vv, q, scale, pos, count, out, lse):
             n = min(max(pos[b] + t + 1, 0), c.T)
             for h in range(H):
                 k, v = kk[b][:, h // grp], vv[b][:, h // grp]
-                ref, rl, A, D = attention(f64(q)[b, t, h], k, v, scale, n)
+                ref, rl, D, bound = attention(f64(q)[b, t, h], k, v, scale, n, c.block)
                 got, gl = f64(out)[b, t, h], float(lse[b, t, h])
                 if n == 0:
                     assert (got == 0).all() and gl == -math.inf
                     continue
-                tol = attention_tolerance(ref, A, D, v, n, name)
+                tol = bound(name)
                 err = np.abs(got - ref)
                 assert (err <= tol).all(), (b, t, h, n, float((err / tol).max()))
                 assert abs(gl - rl) <= lse_tolerance(rl, D), (b, t, h, gl, rl)
@@ -358,9 +358,8 @@ def test_attention_ignores_what_lies_behind():
     ok = f64(q)[:, :2]
     for t in range(2):
         for h in range(4):
-            ref, rl, A, D = attention(ok[0, t, h], np.nan_to_num(val[0][0][:, h // 2]), val[1][0][:, h // 2], 0.125, 31 + t)
-            tol = attention_tolerance(ref, A, D, val[1][0][:, h // 2], 31 + t, "bfloat16")
-            assert (np.abs(f64(out)[0, t, h] - ref) <= tol).all() and abs(float(lse[0, t, h]) - rl) <= lse_tolerance(rl, D)
+            ref, rl, D, bound = attention(ok[0, t, h], np.nan_to_num(val[0][0][:, h // 2]), val[1][0][:, h // 2], 0.125, 31 + t, block)
+            assert (np.abs(f64(out)[0, t, h] - ref) <= bound("bfloat16")).all() and abs(float(lse[0, t, h]) - rl) <= lse_tolerance(rl, D)
 
 
 def test_attention_blocks_of_very_different_scales():
