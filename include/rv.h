@@ -388,7 +388,7 @@ int rv_rope(const rv_rope_plan *plan, const rv_heads *q_in, const rv_heads *q_ou
 #define RV_KV8_INT8 0
 #define RV_KV8_E4M3 1
 typedef struct rv_kv8 {
-  int max_batch, n_kv_heads, head_dim, max_seq; /* head_dim 64 or 128 */
+  int max_batch, n_kv_heads, head_dim, max_seq; /* <= 65535, <= 1024, 64 or 128 */
   int block;     /* 16, 32, 64 or 128 */
   int format;    /* RV_KV8_* */
   int act_dtype; /* RV_F16 or RV_BF16: the type of the originals */

@@ -122,9 +122,9 @@ def test_outputs_whose_rows_overlap_are_refused(kw):
 def test_bad_batches(B, T):
     h = heads()
     refused(rv.rope, rv.rope_plan(128), h, h, None, None, B, T, None)
-    refused(rv.kv8_append, cache(max_batch=1 << 21), h, h, B, T, None)
-    refused(rv.kv8_read, cache(max_batch=1 << 21), h, h, B, T, None)
-    refused(rv.kv8_attention, cache(max_batch=1 << 21), h, h, B, T, 1.0, None, None, None, OK, 1 << 40)
+    refused(rv.kv8_append, cache(max_batch=65535), h, h, B, T, None)
+    refused(rv.kv8_read, cache(max_batch=65535), h, h, B, T, None)
+    refused(rv.kv8_attention, cache(max_batch=65535), h, h, B, T, 1.0, None, None, None, OK, 1 << 40)
 
 
 def test_rope_refusals():
@@ -142,7 +142,7 @@ def test_rope_refusals():
     refused(rv.rope, p, h, h, None, None, 1, 1, None, OK + 1)
 
 
-BAD_CACHES = [dict(max_batch=0), dict(n_kv_heads=0), dict(max_seq=0), dict(max_seq=2 ** 31 - 1), dict(head_dim=96), dict(block=48),
+BAD_CACHES = [dict(max_batch=0), dict(max_batch=65536), dict(n_kv_heads=1025), dict(n_kv_heads=0), dict(max_seq=0), dict(max_seq=2 ** 31 - 1), dict(head_dim=96), dict(block=48),
               dict(block=256), dict(block=0), dict(format=2), dict(act_dtype=rv.F32), dict(k_codes=0), dict(v_codes=0), dict(k_scale=0),
               dict(v_scale=0), dict(k_tail=0), dict(v_tail=0), dict(k_codes=OK + 4), dict(v_tail=OK + 8)]
 

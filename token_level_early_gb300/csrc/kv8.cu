@@ -25,7 +25,11 @@ template <int ACT>
 __device__ __forceinline__ constexpr uint32_t inf_bits() { return ACT == RV_BF16 ? 0x7f80u : 0x7c00u; }
 
 // Largest magnitude bits of the two 16-bit halves of a and b.
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) { return __vmaxu2(a, b & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b & 0x7fff7fffu));
+  return r;
+}
 
 // Scale of a block whose largest magnitude bits are m.
 template <int ACT, int FMT>
@@ -36,12 +40,29 @@ __device__ __forceinline__ float block_scale(uint32_t m) {
   return fmaxf(up, kScaleMin);
 }
 
-// Two codes of a 16-bit pair (low half first), in the low 16 bits.
+// Four codes of two 16-bit pairs.  The quotient x / s is x * inv (inv = 1 / s)
+// with one step of residual correction (Markstein): r = x - t s is exact where
+// x / s is representable, as midpoints between codes are, and t + r inv then
+// rounds to it; elsewhere the result is within a unit in the last place, far
+// from any midpoint.  int8: adding 1.5 2^23 rounds to the nearest integer,
+// ties to even, and leaves it in the low byte.
 template <int ACT, int FMT>
-__device__ __forceinline__ uint32_t code2(uint32_t v, float s) {
-  const float x0 = act_to_f((uint16_t)v, ACT) / s, x1 = act_to_f((uint16_t)(v >> 16), ACT) / s;
-  if (FMT == RV_KV8_INT8) return (uint32_t)(__float2int_rn(x0) & 0xff) | (uint32_t)(__float2int_rn(x1) & 0xff) << 8;
-  return __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+__device__ __forceinline__ uint32_t code4(uint32_t v0, uint32_t v1, float s, float inv) {
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = i < 2 ? v0 : v1;
+    const float x = act_to_f((uint16_t)(i & 1 ? w >> 16 : w), ACT), t = x * inv;
+    y[i] = fmaf(fmaf(-t, s, x), inv, t);
+    if (FMT == RV_KV8_INT8) y[i] += 12582912.f;
+  }
+  if (FMT == RV_KV8_INT8) {
+    const uint32_t a = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    return __byte_perm(a, b, 0x5410);
+  }
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
 // 8 values of an input row as 16-bit pairs (RV_F32 rows are rounded).
@@ -50,172 +71,186 @@ __device__ __forceinline__ uint4 load_row8(const void *base, int64_t off) {
   if (!F32) return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
   const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
   const float4 a = p[0], b = p[1];
-  auto two = [](float x, float y) { return f_to_act(x, ACT) | (uint32_t)f_to_act(y, ACT) << 16; };
-  return make_uint4(two(a.x, a.y), two(a.z, a.w), two(b.x, b.y), two(b.z, b.w));
+  return make_uint4(pack_act2(a.x, a.y, ACT), pack_act2(a.z, a.w, ACT), pack_act2(b.x, b.y, ACT), pack_act2(b.z, b.w, ACT));
 }
 
 // ------------------------------------------------------------------ append
 
-struct AppendGrid {
-  int threads_per_unit, units_per_block;  // a unit is one cache block
-  int blocks_per_row;                     // cache blocks that T tokens can touch
-  int64_t units;
-};
-
-// A unit (threads_per_unit threads, 4 vectors of 8 values each) takes one
-// cache block: originals before the row's first new position come from the
-// tail, the others from the input; their largest magnitude gives the scale,
-// and the codes of the block's present positions are written.  The unit of a
-// row's first block also copies the row's last 2 x block new originals into
-// the tail, after it has read what it needs from there: no other unit reads
-// the tail.
-template <int ACT, int FMT, bool F32, int HD>
-__global__ void k_append(Kv8 c, Kv8Io io, AppendGrid g) {
+// A block of threads takes one cache block of one row, KV head and K or V: NV
+// vectors of 8 values a thread, so block x head_dim / (8 NV) threads.  Originals
+// before the row's first new position come from the tail, the others from the
+// input; their largest magnitude gives the scale, and the codes of the block's
+// present positions are written.  The threads of a row's first block also copy
+// the row's last 2 x block new originals into the tail, after they have read
+// what they need from there: no others read the tail.
+template <int ACT, int FMT, bool F32, int HD, int NV>
+__global__ void __launch_bounds__(512) k_append(Kv8 c, Kv8Io io, int log_block) {
   pdl_wait();
   pdl_trigger();
   constexpr int VR = HD / 8;  // vectors of a row
   __shared__ uint32_t red[16];
-  const int grp = threadIdx.x / g.threads_per_unit, tid = threadIdx.x - grp * g.threads_per_unit;
-  const int64_t unit = (int64_t)blockIdx.x * g.units_per_block + grp;
-  bool live = unit < g.units;
-  int b = 0, h = 0, kv = 0, blk = 0, p0 = 0, end = 0, pos = 0;
-  if (live) {
-    const int i = (int)(unit % g.blocks_per_row);
-    int64_t r = unit / g.blocks_per_row;
-    kv = (int)(r & 1);
-    r >>= 1;
-    h = (int)(r % c.Hkv);
-    b = (int)(r / c.Hkv);
-    pos = row_pos(io.pos, b);
-    const int n = row_count(io.count, b, io.T);
-    if (n == 0) {
-      live = false;
-    } else if (pos < 0 || pos >= c.T) {
-      live = false;
-      if (io.err && i == 0 && tid == 0) atomicOr(io.err, kKv8ErrPos);
-    } else {
-      end = (int)min((int64_t)pos + n, (int64_t)c.T);
-      if (io.err && i == 0 && tid == 0 && end - pos < n) atomicOr(io.err, kKv8ErrPos);
-      blk = pos / c.block + i;
-      p0 = blk * c.block;
-      live = p0 < end;
-    }
+  const int tid = threadIdx.x, b = blockIdx.z, h = blockIdx.y >> 1, kv = blockIdx.y & 1, block = 1 << log_block;
+  const int pos = row_pos(io.pos, b), n = row_count(io.count, b, io.T);
+  if (n == 0) return;
+  const int end = (int)min((int64_t)pos + n, (int64_t)c.T);
+  if (pos < 0 || end - pos < n) {  // not a position of the cache, or some tokens are not
+    if (io.err && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) atomicOr(io.err, kKv8ErrPos);
+    if (pos < 0) return;
   }
+  const int blk = (pos >> log_block) + blockIdx.x, p0 = blk << log_block;
+  if (p0 >= end) return;
   const Heads &in = kv ? io.v : io.k;
   const int64_t row = (int64_t)b * c.Hkv + h;
-  uint16_t *tail = c.tail[kv] + row * 2 * c.block * HD;
-  const int64_t src = b * in.sb + h * in.sh;
-  uint4 v[4];
+  const int d = (tid % VR) * 8, p = p0 + tid / VR, step = block / NV;  // a thread's vectors are `step` positions apart
+  uint16_t *tail = c.tail[kv] + row * (2 << log_block) * HD + d;
+  const int64_t src = b * in.sb + h * in.sh + d;
+  const int wrap = 2 * block - 1;
+  uint4 v[NV];
+  if (p0 >= pos && p0 + block <= end) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) v[k] = load_row8<ACT, F32>(in.p, src + (int64_t)(p + k * step - pos) * in.st);
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int q = p + k * step;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (q < pos) v[k] = *reinterpret_cast<const uint4 *>(tail + (q & wrap) * HD);
+      else if (q < end) v[k] = load_row8<ACT, F32>(in.p, src + (int64_t)(q - pos) * in.st);
+    }
+  }
   uint32_t m = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int u = tid + k * g.threads_per_unit, p = p0 + u / VR, d = (u % VR) * 8;
-    v[k] = make_uint4(0, 0, 0, 0);
-    if (live && p < end)
-      v[k] = p < pos ? *reinterpret_cast<const uint4 *>(tail + (p % (2 * c.block)) * HD + d)
-                     : load_row8<ACT, F32>(in.p, src + (p - pos) * in.st + d);
-    m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[k].x), v[k].y), v[k].z), v[k].w);
-  }
+  for (int k = 0; k < NV; ++k) m = max_abs2(max_abs2(max_abs2(max_abs2(m, v[k].x), v[k].y), v[k].z), v[k].w);
   m = max(m & 0xffffu, m >> 16);
   m = __reduce_max_sync(0xffffffffu, m);
-  const int warp = threadIdx.x >> 5, nw = g.threads_per_unit >> 5;
-  if ((threadIdx.x & 31) == 0) red[warp] = m;
-  __syncthreads();
-  for (int i = 0; i < nw; ++i) m = max(m, red[grp * nw + i]);
-  if (!live) return;
-  const float s = block_scale<ACT, FMT>(m);
+  if (blockDim.x > 32) {
+    if ((tid & 31) == 0) red[tid >> 5] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, red[(tid & 31) & ((blockDim.x >> 5) - 1)]);
+  }
+  const float s = block_scale<ACT, FMT>(m), inv = 1.f / s;
   const bool bad = !(s == s);
-  uint8_t *codes = c.codes[kv] + (row * c.N + p0) * HD;
+  uint8_t *codes = c.codes[kv] + (row * c.N + p) * HD + d;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int u = tid + k * g.threads_per_unit;
-    if (p0 + u / VR >= end) continue;
+  for (int k = 0; k < NV; ++k) {
+    if (p + k * step >= end) continue;
     uint2 o = make_uint2(0, 0);
     if (!bad) {
-      o.x = code2<ACT, FMT>(v[k].x, s) | code2<ACT, FMT>(v[k].y, s) << 16;
-      o.y = code2<ACT, FMT>(v[k].z, s) | code2<ACT, FMT>(v[k].w, s) << 16;
+      o.x = code4<ACT, FMT>(v[k].x, v[k].y, s, inv);
+      o.y = code4<ACT, FMT>(v[k].z, v[k].w, s, inv);
     }
-    *reinterpret_cast<uint2 *>(codes + (int64_t)u * 8) = o;
+    *reinterpret_cast<uint2 *>(codes + k * step * HD) = o;
   }
-  if (tid == 0) c.scale[kv][row * (c.N / c.block) + blk] = s;
-  if (p0 <= pos) {
-    const int from = max(pos, end - 2 * c.block);
-    for (int u = tid; u < (end - from) * VR; u += g.threads_per_unit) {
-      const int p = from + u / VR, d = (u % VR) * 8;
-      *reinterpret_cast<uint4 *>(tail + (p % (2 * c.block)) * HD + d) = load_row8<ACT, F32>(in.p, src + (int64_t)(p - pos) * in.st + d);
-    }
+  if (tid == 0) c.scale[kv][row * (c.N >> log_block) + blk] = s;
+  if (blockIdx.x == 0) {
+    const int from = max(pos, end - 2 * block);
+    for (int q = from + tid / VR; q < end; q += step)
+      *reinterpret_cast<uint4 *>(tail + (q & wrap) * HD) = load_row8<ACT, F32>(in.p, src + (int64_t)(q - pos) * in.st);
   }
 }
 
 template <int ACT, int FMT, bool F32, int HD>
 cudaError_t append_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s, int pdl) {
-  AppendGrid g;
-  g.threads_per_unit = c.block * HD / 32;
-  const int threads = g.threads_per_unit < 128 ? 128 : g.threads_per_unit;
-  g.units_per_block = threads / g.threads_per_unit;
-  g.blocks_per_row = (io.T + c.block - 2) / c.block + 1;
-  g.units = (int64_t)g.blocks_per_row * 2 * c.Hkv * io.B;
-  const int64_t grid = (g.units + g.units_per_block - 1) / g.units_per_block;
-  if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_k(k_append<ACT, FMT, F32, HD>, dim3((unsigned)grid), dim3(threads), 0, s, pdl, c, io, g);
+  int log_block = 4;
+  while (1 << log_block < c.block) ++log_block;
+  const dim3 grid((io.T + c.block - 2) / c.block + 1, 2 * c.Hkv, io.B);  // blocks that T positions can touch
+  // 4 vectors a thread where a call is short and its latency counts (or a
+  // block has no more), 8 where it is long and a thread's fixed work counts
+  if (io.T > 2 * c.block && c.block * HD >= 2048)
+    return launch_k(k_append<ACT, FMT, F32, HD, 8>, grid, dim3(c.block * HD / 64), 0, s, pdl, c, io, log_block);
+  return launch_k(k_append<ACT, FMT, F32, HD, 4>, grid, dim3(c.block * HD / 32), 0, s, pdl, c, io, log_block);
 }
 
 // ------------------------------------------------------------------ read
 
-// One thread reads 8 codes of a row and writes their values.
-template <int OUT, int FMT, int HD>
-__global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, int64_t total) {
-  constexpr int VR = HD / 8;
-  for (int64_t u = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; u < total; u += (int64_t)gridDim.x * blockDim.x) {
-    const int d = (int)(u % VR) * 8;
-    int64_t r = u / VR;
-    const int h = (int)(r % c.Hkv);
-    r /= c.Hkv;
-    const int t = (int)(r % io.T);
-    r /= io.T;
-    const int b = (int)(r % io.B), kv = (int)(r / io.B);
-    const Heads &out = kv ? io.v : io.k;
-    if (!out.p || t >= row_count(io.count, b, io.T)) continue;
-    const int64_t p = (int64_t)row_pos(io.pos, b) + t;
-    if (p < 0 || p >= c.T) {
-      if (io.err) atomicOr(io.err, kKv8ErrPos);
-      continue;
-    }
-    const int64_t row = (int64_t)b * c.Hkv + h;
-    const uint2 w = *reinterpret_cast<const uint2 *>(c.codes[kv] + (row * c.N + p) * HD + d);
-    const float s = c.scale[kv][row * (c.N / c.block) + p / c.block];
-    const uint32_t cw[2] = {w.x, w.y};
-    float x[8];
+// 16 codes -> values of the output type, rounded once.  A block whose largest
+// possible value passes the type's range is limited to it.
+template <int OUT, int FMT>
+__device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst) {
+  const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
+  float x[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint8_t q = (uint8_t)(cw[i >> 2] >> (8 * (i & 3)));
-      x[i] = FMT == RV_KV8_INT8 ? (float)(int8_t)q : __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
-      x[i] *= s;
-    }
-    const int64_t dst = b * out.sb + t * out.st + h * out.sh + d;
-    if (OUT == RV_F32) {
-      float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out.p) + dst);
-      o[0] = make_float4(x[0], x[1], x[2], x[3]);
-      o[1] = make_float4(x[4], x[5], x[6], x[7]);
+  for (int i = 0; i < 4; ++i) {
+    __half2 lo, hi;
+    if (FMT == RV_KV8_INT8) {  // byte ^ 0x80 = code + 128 under the exponent of 1024 is 1152 + code
+      const uint32_t u = cw[i] ^ 0x80808080u, a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+      const __half2 bias = __half2half2(__ushort_as_half(0x6480));
+      lo = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+      hi = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
     } else {
-      const float top = OUT == RV_F16 ? 65504.f : __uint_as_float(0x7f7f0000u);
-      uint32_t o[4];
+      lo = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)cw[i], __NV_E4M3));
+      hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[i] >> 16), __NV_E4M3));
+    }
+    const float2 f = __half22float2(lo), g = __half22float2(hi);
+    x[4 * i] = f.x * s; x[4 * i + 1] = f.y * s; x[4 * i + 2] = g.x * s; x[4 * i + 3] = g.y * s;
+  }
+  if (OUT == RV_F32) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + dst);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (x[i] == x[i]) x[i] = fminf(fmaxf(x[i], -top), top);
+    for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else {
+    const float top = OUT == RV_F16 ? 65504.f : __uint_as_float(0x7f7f0000u);
+    if (s * (FMT == RV_KV8_INT8 ? 127.f : 448.f) > top) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = f_to_act(x[2 * i], OUT) | (uint32_t)f_to_act(x[2 * i + 1], OUT) << 16;
-      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out.p) + dst) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -top), top);
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = pack_act2(x[2 * i], x[2 * i + 1], OUT);
+    uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + dst);
+    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+// A block takes a run of one row's tokens and up to 256 / (HD / 16) heads of
+// K or V; a thread keeps its 16 elements of one head and goes from token to
+// token, four loads in flight.
+constexpr int kReadItems = 4;
+struct ReadGrid {
+  int heads, groups;  // heads of a block, blocks of all heads
+};
+template <int OUT, int FMT, int HD>
+__global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
+  constexpr int CH = HD / 16;
+  const int kv = blockIdx.y & 1, per = g.heads * CH, pass = blockDim.x / per, b = blockIdx.z;  // tokens of a pass
+  const Heads &out = kv ? io.v : io.k;
+  const int t0 = blockIdx.x * pass * kReadItems, t1 = min(row_count(io.count, b, io.T), t0 + pass * kReadItems);
+  if (!out.p || t0 >= t1) return;
+  const int pos = row_pos(io.pos, b), shift = __ffs(c.block) - 1;
+  if (io.err && threadIdx.x == 0 && ((int64_t)pos + t0 < 0 || (int64_t)pos + t1 > c.T)) atomicOr(io.err, kKv8ErrPos);
+  const int tl = threadIdx.x / per, r = threadIdx.x - tl * per, h = (blockIdx.y >> 1) * g.heads + r / CH, d = r % CH * 16;
+  if (h >= c.Hkv) return;
+  const int64_t row = (int64_t)b * c.Hkv + h, p0 = (int64_t)pos + t0 + tl;
+  const uint8_t *src = c.codes[kv] + (row * c.N + p0) * HD + d;
+  const float *scale = c.scale[kv] + row * (c.N >> shift);
+  const int64_t dst = b * out.sb + (int64_t)(t0 + tl) * out.st + h * out.sh + d, step = pass * out.st;
+  uint4 w[kReadItems];
+  float s[kReadItems];
+  bool ok[kReadItems];
+#pragma unroll
+  for (int k = 0; k < kReadItems; ++k) {
+    const int64_t p = p0 + k * pass;
+    ok[k] = t0 + tl + k * pass < t1 && p >= 0 && p < c.T;
+    if (ok[k]) {
+      w[k] = __ldg(reinterpret_cast<const uint4 *>(src + k * pass * HD));
+      s[k] = __ldg(scale + (p >> shift));
     }
   }
+#pragma unroll
+  for (int k = 0; k < kReadItems; ++k)
+    if (ok[k]) read16<OUT, FMT>(w[k], s[k], out.p, dst + k * step);
 }
 
 template <int OUT, int FMT>
 cudaError_t read_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s) {
-  const int64_t total = (int64_t)2 * io.B * io.T * c.Hkv * (c.hd / 8);
-  const int64_t grid = (total + 255) / 256;
+  const int chunks = c.hd / 16, most = 256 / chunks;
+  ReadGrid g;
+  g.heads = c.Hkv < most ? c.Hkv : most;
+  g.groups = (c.Hkv + g.heads - 1) / g.heads;
+  const int per = g.heads * chunks, pass = 256 / per, tokens = pass * kReadItems;
   auto fn = c.hd == 64 ? k_read<OUT, FMT, 64> : k_read<OUT, FMT, 128>;
-  fn<<<(unsigned)(grid < 152 * 64 ? grid : 152 * 64), 256, 0, s>>>(c, io, total);
+  fn<<<dim3((io.T + tokens - 1) / tokens, 2 * g.groups, io.B), pass * per, 0, s>>>(c, io, g);
   return cudaGetLastError();
 }
 
@@ -265,8 +300,8 @@ namespace {
 
 int check_cache(const rv_kv8 *c, bool pointers) {
   if (!c) return op_fail(RV_EINVAL, "null pointer");
-  if (c->max_batch < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 65535 || c->max_seq < 1)
-    return op_fail(RV_EINVAL, "cache: max_batch, n_kv_heads and max_seq must be positive");
+  if (c->max_batch < 1 || c->max_batch > 65535 || c->n_kv_heads < 1 || c->n_kv_heads > 1024 || c->max_seq < 1)
+    return op_fail(RV_EINVAL, "cache: max_batch in 1..65535, n_kv_heads in 1..1024 and max_seq > 0 are needed");
   if (c->max_seq > INT32_MAX - 256) return op_fail(RV_EINVAL, "cache: max_seq too large");
   if (c->head_dim != 64 && c->head_dim != 128) return op_fail(RV_EINVAL, "cache: head_dim must be 64 or 128");
   if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128)
@@ -285,6 +320,8 @@ int check_cache(const rv_kv8 *c, bool pointers) {
 int check_rows(const rv_kv8 *c, int B, int T) {
   if (check_batch(B, T)) return RV_EINVAL;
   if (B > c->max_batch) return op_fail(RV_EINVAL, "B above the cache's max_batch");
+  // what the launches count in 32 bits: 16-token blocks of both K and V of every head
+  if (((int64_t)T / 16 + 2) * B * 2 * c->n_kv_heads > INT32_MAX) return op_fail(RV_EINVAL, "B x T x n_kv_heads too large");
   return RV_OK;
 }
 

@@ -211,7 +211,7 @@ __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, in
     *reinterpret_cast<float4 *>(static_cast<float *>(a.out.p) + o) = x;
   } else {
     *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out.p) + o) =
-        make_uint2(f_to_act(x.x, act) | (uint32_t)f_to_act(x.y, act) << 16, f_to_act(x.z, act) | (uint32_t)f_to_act(x.w, act) << 16);
+        make_uint2(pack_act2(x.x, x.y, act), pack_act2(x.z, x.w, act));
   }
   if (a.lse && d == 0) a.lse[((int64_t)b * a.T + t) * a.H + h] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
 }

@@ -30,6 +30,14 @@ struct FastDiv {
 inline FastDiv fast_div(uint32_t d) { return FastDiv{d, d == 1 ? 0u : (uint32_t)((1ull << 32) / d + 1)}; }
 __device__ __forceinline__ uint32_t div_by(uint32_t x, FastDiv f) { return f.d == 1 ? x : __umulhi(x, f.m); }
 
+// Two floats rounded to a 16-bit pair (lo in the low half).
+__device__ __forceinline__ uint32_t pack_act2(float lo, float hi, int act) {
+  uint32_t r;
+  if (act) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // A row's token count and first position (see the conventions in rv.h).
 __device__ __forceinline__ int row_count(const int32_t *count, int b, int T) {
   return count ? min(max(__ldg(count + b), 0), T) : T;

@@ -85,17 +85,35 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 8 elements of a row <-> floats.
+// 8 elements of a row as they lie in memory, and as floats.
 template <int DT>
-__device__ __forceinline__ void load8(const void *base, int64_t off, float (&x)[8]) {
+struct Raw8 {
+  uint4 v[DT == RV_F32 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const void *base, int64_t off) {
+  Raw8<DT> r;
   if (DT == RV_F32) {
-    const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + off);
-    const float4 a = p[0], b = p[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + off);
+    r.v[0] = p[0];
+    r.v[DT == RV_F32] = p[DT == RV_F32];
   } else {
-    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    r.v[0] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + off);
+  }
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void floats8(const Raw8<DT> &r, float (&x)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+  if (DT == RV_F32) {
+    const uint4 h = r.v[DT == RV_F32];
+    const uint32_t y[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = __uint_as_float(w[i]);
+      x[4 + i] = __uint_as_float(y[i]);
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = act_to_f((uint16_t)w[i], DT);
@@ -111,10 +129,8 @@ __device__ __forceinline__ void store8(void *base, int64_t off, const float (&x)
     p[0] = make_float4(x[0], x[1], x[2], x[3]);
     p[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f_to_act(x[2 * i], DT) | (uint32_t)f_to_act(x[2 * i + 1], DT) << 16;
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) =
+        make_uint4(pack_act2(x[0], x[1], DT), pack_act2(x[2], x[3], DT), pack_act2(x[4], x[5], DT), pack_act2(x[6], x[7], DT));
   }
 }
 
@@ -128,74 +144,124 @@ __device__ __forceinline__ float2 cos_sin(int64_t p, uint64_t turns) {
 
 struct RopeGrid {
   int tokens_per_block;
-  FastDiv items, chunks, pairs;  // items of a token, 8-pair chunks of a head, pairs
+  FastDiv items, chunks, pairs, row;  // items of a token, 16-element chunks of a head, pairs, tokens of a row
 };
 
-// One item: 8 pairs (16 elements) of one head of one token.
+// One item: 16 elements (8 pairs) of one head of one token.
+struct Item {
+  bool ok, rot;
+  int which, cs;             // q or k; first of its 8 pairs in the block's table
+  int64_t src, dst;
+  int lo, hi;                // the two runs of 8 elements
+};
+
+// A block takes a run of tokens: its threads ask for their first kItems items,
+// make the tokens' sines and cosines while these are on the way, then turn
+// and store them.
 template <int IN, int OUT, bool HALF>
-__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ rv_rope_plan plan, RopeArgs a, RopeGrid g) {
+__global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ rv_rope_plan plan, const __grid_constant__ RopeArgs a, RopeGrid g) {
+  constexpr int kItems = IN == RV_F32 ? 2 : 4;
   extern __shared__ float2 cs[];  // [tokens_per_block][pairs]
   const int pairs = plan.rotary_dim / 2, tok0 = blockIdx.x * g.tokens_per_block;
-  const int ntok = min(g.tokens_per_block, a.B * a.T - tok0);
+  const int ntok = min(g.tokens_per_block, a.B * a.T - tok0), b0 = tok0 / a.T, at0 = tok0 - b0 * a.T;
+  const int per = g.items.d, total = ntok * per;
+  // row and token of the block's token tk (the quotient is exact below 2^16; above, at most one row ends)
+  auto place = [&](int tk, int &b, int &t) {
+    const int x = at0 + tk, q = a.T < 32768 ? (int)div_by(x, g.row) : x >= a.T;
+    b = b0 + q;
+    t = x - q * a.T;
+  };
+  auto item = [&](int it) {
+    Item m;
+    const int tk = div_by(it, g.items), r = it - tk * per;
+    const int hh = div_by(r, g.chunks), j = r - hh * (int)g.chunks.d;
+    int b, t;
+    place(tk, b, t);
+    m.ok = it < total && t < row_count(a.count, b, a.T);
+    m.which = hh >= a.H[0];
+    const int h = hh - (m.which ? a.H[0] : 0);
+    m.rot = 16 * j < plan.rotary_dim;
+    m.cs = tk * pairs + 8 * j;
+    m.lo = m.rot && HALF ? 8 * j : 16 * j;
+    m.hi = m.rot && HALF ? m.lo + pairs : m.lo + 8;
+    const Heads &in = a.in[m.which], &out = a.out[m.which];
+    m.src = b * in.sb + t * in.st + h * in.sh;
+    m.dst = b * out.sb + t * out.st + h * out.sh;
+    return m;
+  };
+  auto turn = [&](const Item &m, const Raw8<IN> &rx, const Raw8<IN> &ry) {
+    float x[8], y[8];
+    floats8<IN>(rx, x);
+    floats8<IN>(ry, y);
+    if (m.rot) {
+      float2 c[8];
+      const float4 *p = reinterpret_cast<const float4 *>(cs + m.cs);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = p[i];
+        c[2 * i] = make_float2(v.x, v.y);
+        c[2 * i + 1] = make_float2(v.z, v.w);
+      }
+      auto pair = [](float &x0, float &x1, float2 c) {
+        const float u = x0 * c.x - x1 * c.y, v = x0 * c.y + x1 * c.x;
+        x0 = u;
+        x1 = v;
+      };
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (HALF) pair(x[i], y[i], c[i]);
+        else if (i < 4) pair(x[2 * i], x[2 * i + 1], c[i]);
+        else pair(y[2 * i - 8], y[2 * i - 7], c[i]);
+      }
+    }
+    store8<OUT>(a.out[m.which].p, m.dst + m.lo, x);
+    store8<OUT>(a.out[m.which].p, m.dst + m.hi, y);
+  };
+
+  Item m[kItems];
+  Raw8<IN> x[kItems], y[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    m[k] = item(threadIdx.x + k * kThreads);
+    if (m[k].ok) {
+      x[k] = load8<IN>(a.in[m[k].which].p, m[k].src + m[k].lo);
+      y[k] = load8<IN>(a.in[m[k].which].p, m[k].src + m[k].hi);
+    }
+  }
   for (int u = threadIdx.x; u < ntok * pairs; u += kThreads) {
-    const int tk = div_by(u, g.pairs), i = u - tk * pairs, tok = tok0 + tk;
-    const int b = tok / a.T;
-    float2 v = cos_sin((int64_t)row_pos(a.pos, b) + (tok - b * a.T), plan.turns[i]);
+    const int tk = div_by(u, g.pairs), i = u - tk * pairs;
+    int b, t;
+    place(tk, b, t);
+    float2 v = cos_sin((int64_t)row_pos(a.pos, b) + t, plan.turns[i]);
     v.x *= plan.attention_factor;
     v.y *= a.inverse ? -plan.attention_factor : plan.attention_factor;
     cs[u] = v;
   }
   __syncthreads();
-  const int per = g.items.d, total = ntok * per;
-  for (int it = threadIdx.x; it < total; it += kThreads) {
-    const int tk = div_by(it, g.items), r = it - tk * per;
-    const int hh = div_by(r, g.chunks), j = r - hh * (int)g.chunks.d;
-    const int tok = tok0 + tk, b = tok / a.T, t = tok - b * a.T;
-    if (t >= row_count(a.count, b, a.T)) continue;
-    const int which = hh >= a.H[0], h = hh - (which ? a.H[0] : 0);
-    const bool rot = 16 * j < plan.rotary_dim;
-    const Heads &in = a.in[which], &out = a.out[which];
-    const int lo = rot && HALF ? 8 * j : 16 * j, hi = rot && HALF ? lo + pairs : lo + 8;
-    const int64_t src = b * in.sb + t * in.st + h * in.sh, dst = b * out.sb + t * out.st + h * out.sh;
-    float x[8], y[8];
-    load8<IN>(in.p, src + lo, x);
-    load8<IN>(in.p, src + hi, y);
-    if (rot) {
-      const float2 *c = cs + tk * pairs + 8 * j;
-      if (HALF) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x0 = x[i], x1 = y[i];
-          x[i] = x0 * c[i].x - x1 * c[i].y;
-          y[i] = x0 * c[i].y + x1 * c[i].x;
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float x0 = x[2 * i], x1 = x[2 * i + 1];
-          x[2 * i] = x0 * c[i].x - x1 * c[i].y;
-          x[2 * i + 1] = x0 * c[i].y + x1 * c[i].x;
-          x0 = y[2 * i], x1 = y[2 * i + 1];
-          y[2 * i] = x0 * c[i + 4].x - x1 * c[i + 4].y;
-          y[2 * i + 1] = x0 * c[i + 4].y + x1 * c[i + 4].x;
-        }
-      }
-    }
-    store8<OUT>(out.p, dst + lo, x);
-    store8<OUT>(out.p, dst + hi, y);
+  for (int k = 0; k < kItems; ++k)
+    if (m[k].ok) turn(m[k], x[k], y[k]);
+  for (int it = threadIdx.x + kItems * kThreads; it < total; it += kThreads) {  // heads beyond a block's items
+    const Item n = item(it);
+    if (n.ok) turn(n, load8<IN>(a.in[n.which].p, n.src + n.lo), load8<IN>(a.in[n.which].p, n.src + n.hi));
   }
 }
 
 template <int IN, int OUT>
 cudaError_t launch_io(const rv_rope_plan &plan, const RopeArgs &a, cudaStream_t s) {
-  const int chunks = plan.head_dim / 16, items = (a.H[0] + a.H[1]) * chunks, pairs = plan.rotary_dim / 2;
+  const int chunks = plan.head_dim / 16, items = (a.H[0] + a.H[1]) * chunks, pairs = plan.rotary_dim / 2, tokens = a.B * a.T;
   RopeGrid g;
-  g.tokens_per_block = 1;
+  // as many tokens as the threads' first items cover, but enough blocks to fill the GPU
+  int tpb = kThreads * (IN == RV_F32 ? 2 : 4) / items;
+  if (tpb > tokens / 608) tpb = tokens / 608;
+  if (tpb < 1) tpb = 1;
+  g.tokens_per_block = tpb;
   g.items = fast_div(items);
   g.chunks = fast_div(chunks);
   g.pairs = fast_div(pairs);
-  const int grid = (a.B * a.T + g.tokens_per_block - 1) / g.tokens_per_block;
-  const size_t smem = sizeof(float2) * pairs * g.tokens_per_block;
+  g.row = fast_div(a.T);
+  const int grid = (tokens + tpb - 1) / tpb;
+  const size_t smem = sizeof(float2) * pairs * tpb;
   auto fn = plan.layout == RV_ROPE_HALF ? k_rope<IN, OUT, true> : k_rope<IN, OUT, false>;
   fn<<<grid, kThreads, smem, s>>>(plan, a, g);
   return cudaGetLastError();
