@@ -47,22 +47,23 @@ __device__ __forceinline__ float block_scale(uint32_t m) {
 // from any midpoint.  int8: adding 1.5 2^23 rounds to the nearest integer,
 // ties to even, and leaves it in the low byte.
 template <int ACT, int FMT>
-__device__ __forceinline__ uint32_t code4(uint32_t v0, uint32_t v1, float s, float inv) {
-  float y[4];
+__device__ __forceinline__ uint32_t code4(uint32_t v0, uint32_t v1, F2 neg_s, F2 inv) {
+  float2 y[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = i < 2 ? v0 : v1;
-    const float x = act_to_f((uint16_t)(i & 1 ? w >> 16 : w), ACT), t = x * inv;
-    y[i] = fmaf(fmaf(-t, s, x), inv, t);
-    if (FMT == RV_KV8_INT8) y[i] += 12582912.f;
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w = i ? v1 : v0;
+    const F2 x = f2(act_to_f((uint16_t)w, ACT), act_to_f((uint16_t)(w >> 16), ACT)), t = f2_mul(x, inv);
+    F2 q = f2_fma(f2_fma(t, neg_s, x), inv, t);
+    if (FMT == RV_KV8_INT8) q = f2_add(q, f2(12582912.f, 12582912.f));
+    y[i] = f2_split(q);
   }
   if (FMT == RV_KV8_INT8) {
-    const uint32_t a = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x0040);
-    const uint32_t b = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x0040);
+    const uint32_t a = __byte_perm(__float_as_uint(y[0].x), __float_as_uint(y[0].y), 0x0040);
+    const uint32_t b = __byte_perm(__float_as_uint(y[1].x), __float_as_uint(y[1].y), 0x0040);
     return __byte_perm(a, b, 0x5410);
   }
-  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3) |
-         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(y[0], __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(y[1], __NV_SATFINITE, __NV_E4M3) << 16;
 }
 
 // 8 values of an input row as 16-bit pairs (RV_F32 rows are rounded).
@@ -105,10 +106,13 @@ __global__ void __launch_bounds__(512) k_append(Kv8 c, Kv8Io io, int log_block) 
   uint16_t *tail = c.tail[kv] + row * (2 << log_block) * HD + d;
   const int64_t src = b * in.sb + h * in.sh + d;
   const int wrap = 2 * block - 1;
+  const int64_t src_step = (int64_t)step * in.st;
+  const bool all = p0 + block <= end;
   uint4 v[NV];
-  if (p0 >= pos && p0 + block <= end) {
+  if (p0 >= pos && all) {
+    int64_t o = src + (int64_t)(p - pos) * in.st;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) v[k] = load_row8<ACT, F32>(in.p, src + (int64_t)(p + k * step - pos) * in.st);
+    for (int k = 0; k < NV; ++k, o += src_step) v[k] = load_row8<ACT, F32>(in.p, o);
   } else {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -130,16 +134,14 @@ __global__ void __launch_bounds__(512) k_append(Kv8 c, Kv8Io io, int log_block) 
   }
   const float s = block_scale<ACT, FMT>(m), inv = 1.f / s;
   const bool bad = !(s == s);
+  const F2 ns2 = f2(-s, -s), inv2 = f2(inv, inv);
   uint8_t *codes = c.codes[kv] + (row * c.N + p) * HD + d;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (p + k * step >= end) continue;
-    uint2 o = make_uint2(0, 0);
-    if (!bad) {
-      o.x = code4<ACT, FMT>(v[k].x, v[k].y, s, inv);
-      o.y = code4<ACT, FMT>(v[k].z, v[k].w, s, inv);
-    }
-    *reinterpret_cast<uint2 *>(codes + k * step * HD) = o;
+  for (int k = 0; k < NV; ++k, codes += step * HD) {
+    if (!all && p + k * step >= end) continue;
+    uint2 o = make_uint2(code4<ACT, FMT>(v[k].x, v[k].y, ns2, inv2), code4<ACT, FMT>(v[k].z, v[k].w, ns2, inv2));
+    if (bad) o = make_uint2(0, 0);
+    *reinterpret_cast<uint2 *>(codes) = o;
   }
   if (tid == 0) c.scale[kv][row * (c.N >> log_block) + blk] = s;
   if (blockIdx.x == 0) {
@@ -163,10 +165,24 @@ cudaError_t append_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s, int pdl) {
 
 // ------------------------------------------------------------------ read
 
+// 32 bytes in one store where they lie on a 32-byte boundary: two 16-byte
+// stores of a warp would each write half sectors.
+__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                 "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    uint4 *d = static_cast<uint4 *>(p);
+    d[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    d[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
 // 16 codes -> values of the output type, rounded once.  A block whose largest
 // possible value passes the type's range is limited to it.
 template <int OUT, int FMT>
-__device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst) {
+__device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst, bool wide) {
   const uint32_t cw[4] = {w.x, w.y, w.z, w.w};
   float x[16];
 #pragma unroll
@@ -182,12 +198,15 @@ __device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst)
       hi = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(cw[i] >> 16), __NV_E4M3));
     }
     const float2 f = __half22float2(lo), g = __half22float2(hi);
-    x[4 * i] = f.x * s; x[4 * i + 1] = f.y * s; x[4 * i + 2] = g.x * s; x[4 * i + 3] = g.y * s;
+    const float2 u = f2_split(f2_mul(f2(f.x, f.y), f2(s, s))), v = f2_split(f2_mul(f2(g.x, g.y), f2(s, s)));
+    x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = v.x; x[4 * i + 3] = v.y;
   }
   if (OUT == RV_F32) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + dst);
+    uint32_t o[2][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < 16; ++i) o[i >> 3][i & 7] = __float_as_uint(x[i]);
+    store32(static_cast<float *>(out) + dst, o[0], wide);
+    store32(static_cast<float *>(out) + dst + 8, o[1], wide);
   } else {
     const float top = OUT == RV_F16 ? 65504.f : __uint_as_float(0x7f7f0000u);
     if (s * (FMT == RV_KV8_INT8 ? 127.f : 448.f) > top) {
@@ -197,9 +216,7 @@ __device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst)
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i] = pack_act2(x[2 * i], x[2 * i + 1], OUT);
-    uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + dst);
-    d[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    d[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    store32(static_cast<uint16_t *>(out) + dst, o, wide);
   }
 }
 
@@ -209,6 +226,7 @@ __device__ __forceinline__ void read16(uint4 w, float s, void *out, int64_t dst)
 constexpr int kReadItems = 4;
 struct ReadGrid {
   int heads, groups;  // heads of a block, blocks of all heads
+  bool wide;          // output rows on 32-byte boundaries
 };
 template <int OUT, int FMT, int HD>
 __global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
@@ -239,7 +257,7 @@ __global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
   }
 #pragma unroll
   for (int k = 0; k < kReadItems; ++k)
-    if (ok[k]) read16<OUT, FMT>(w[k], s[k], out.p, dst + k * step);
+    if (ok[k]) read16<OUT, FMT>(w[k], s[k], out.p, dst + k * step, g.wide);
 }
 
 template <int OUT, int FMT>
@@ -248,6 +266,11 @@ cudaError_t read_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s) {
   ReadGrid g;
   g.heads = c.Hkv < most ? c.Hkv : most;
   g.groups = (c.Hkv + g.heads - 1) / g.heads;
+  g.wide = true;
+  for (const Heads *h : {&io.k, &io.v})
+    if (((reinterpret_cast<uintptr_t>(h->p) | (uintptr_t)h->sb * (OUT == RV_F32 ? 4 : 2) | (uintptr_t)h->st * (OUT == RV_F32 ? 4 : 2) |
+          (uintptr_t)h->sh * (OUT == RV_F32 ? 4 : 2)) & 31u))
+      g.wide = false;
   const int per = g.heads * chunks, pass = 256 / per, tokens = pass * kReadItems;
   auto fn = c.hd == 64 ? k_read<OUT, FMT, 64> : k_read<OUT, FMT, 128>;
   fn<<<dim3((io.T + tokens - 1) / tokens, 2 * g.groups, io.B), pass * per, 0, s>>>(c, io, g);
