@@ -34,6 +34,9 @@
 
 #include "ops.cuh"
 
+#ifndef KUT
+#define KUT 8
+#endif
 namespace rv {
 namespace kv8a {
 
@@ -44,14 +47,22 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Smallest piece of the line a block takes: one tile for each of its warps.
 constexpr int kMinTiles = kWarps;
+// What beginning a unit costs a block, in tiles (its queries' operands, the
+// join of the warps): the line counts it, where pieces are long enough.
+constexpr int kUnitTiles = KUT;
 
 // Blocks per SM: as many as the registers leave room for.
 __host__ __device__ constexpr int blocks_per_sm(int hd, int nt) { return nt == 1 && hd == 64 ? 3 : 2; }
-// Tiles of a warp's ring: what the blocks of an SM fit into 227 KB.
-__host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 2 : 3; }
+constexpr int kStages = 2;  // tiles of a warp's ring
 // A stage: K rows, V rows, a K and a V scale for each 16 positions.
 __host__ __device__ constexpr int stage_bytes(int hd) { return 2 * tile_len(hd) * hd + 32; }
-__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return kWarps * stages(nt) * stage_bytes(hd); }
+__host__ __device__ constexpr int ring_bytes(int hd) { return kWarps * kStages * stage_bytes(hd); }
+// The warps' O at a unit's end, in two halves where a whole one is too large.
+__host__ __device__ constexpr int halves(int hd, int nt) { return hd * nt > 256 ? 2 : 1; }
+__host__ __device__ constexpr int state_bytes(int hd, int nt) { return kWarps * 8 * nt * (hd / halves(hd, nt)) * 4; }
+// Query operands in shared memory (more than 8 rows; else in registers).
+__host__ __device__ constexpr int query_bytes(int hd, int nt) { return nt == 1 ? 0 : nt * (hd / 16) * 32 * 8; }
+__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd) + state_bytes(hd, nt) + query_bytes(hd, nt); }
 // One cut unit's state: O [rows][hd], then m and l [rows].
 __host__ __device__ constexpr size_t slot_floats(int hd, int nt) { return (size_t)8 * nt * (hd + 2); }
 
@@ -82,17 +93,7 @@ __device__ __forceinline__ Row row_of(const Kv8AttnArgs &a, int b, int rows_per_
   r.tiles = r.groups ? (r.n + tile_len(HD) - 1) / tile_len(HD) : 0;
   return r;
 }
-__device__ __forceinline__ int64_t line_tiles(const Kv8AttnArgs &a, const Row &r) { return (int64_t)a.c.Hkv * r.groups * r.tiles; }
-__device__ __forceinline__ int64_t piece_of(int64_t total, int blocks) {
-  const int64_t p = (total + blocks - 1) / blocks;
-  return p < kMinTiles ? kMinTiles : p;
-}
-
-__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+__device__ __forceinline__ int row_units(const Kv8AttnArgs &a, const Row &r) { return r.tiles ? a.c.Hkv * r.groups : 0; }
 
 // ------------------------------------------------------------------ operands
 
@@ -171,6 +172,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
   return h2_bits(__floats2half2_rn(lo, hi));
 }
@@ -218,25 +225,32 @@ __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, in
 
 // Query rows of a unit are T x (H / Hkv), token-major: row i is token i / grp,
 // head g grp + i % grp; a row group is 8 NT of them.
+// A segment of the line: tiles [t0, t1) of one unit.
+struct Segment {
+  int b, g, row0, t0, t1;
+  int n, count, tiles;  // the row's visible positions and tokens, the unit's tiles
+  int last_piece;       // the piece that the unit ends in
+  int64_t rows;         // KV row: b Hkv + g
+};
+
 // GS: 16-position steps of a tile that share a scale (the smaller of block and
 // tile).  LO: the weights enter as two fp16 terms (high and low part).
 template <int FMT, int HD, int NT, int GS, bool LO>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(const __grid_constant__ Kv8AttnArgs a, int by_unit) {
-  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = stages(NT), SB = stage_bytes(HD);
+  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = kStages, SB = stage_bytes(HD);
   constexpr int TL = tile_len(HD), TM = TL / 16, NG = TM / GS;
+  constexpr bool QS = NT > 1;  // query operands in shared memory
   extern __shared__ __align__(128) unsigned char sm[];
-  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS];
-  __shared__ int64_t s_scan[kWarps + 1];
+  __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_rs[ROWS], s_qb[ROWS];
+  __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
   __shared__ int s_row;
-  __shared__ int64_t s_at;
   pdl_wait();
-  pdl_trigger();  // after the wait: the joining kernel may read d_pos at once
+  pdl_trigger();  // after the wait: the joining kernel may read d_count at once
   const Kv8 &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
-  const int grp = a.H / c.Hkv;
+  const int grp = a.H / c.Hkv, groups = (a.T * grp + ROWS - 1) / ROWS;
   Cut *cuts = static_cast<Cut *>(a.work);
   float *slots = reinterpret_cast<float *>(cuts + gridDim.x) + (size_t)2 * blockIdx.x * slot_floats(HD, NT);
-  const int groups = (a.T * grp + ROWS - 1) / ROWS;
   if (tid == 0 && !by_unit) cuts[blockIdx.x].last = 0;
   // rows that see nothing have no tiles: zeros
   for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
@@ -251,203 +265,269 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     }
   }
 
-  // ---- this block's piece of the line
-  int64_t total, piece, begin, end;
-  int b;
-  int64_t off;  // tiles of row b that lie before the piece
-  if (a.B == 1) {
-    total = line_tiles(a, row_of<HD>(a, 0, ROWS));
-    piece = piece_of(total, gridDim.x);
-    begin = piece * blockIdx.x;
-    if (begin >= total) return;
-    end = min(total, begin + piece);
-    b = 0;
-    off = begin;
-  } else {
-    // each thread sums a run of rows; the thread whose run holds the piece's
-    // begin finds the row
+  // ---- this block's piece [begin, end) of the line, and where it begins:
+  // `off` into row `b`.  A unit takes `extra` + its tiles of the line.
+  int64_t total, piece, begin, end, off = 0;
+  int b = 0, extra;
+  {
+    // each thread sums a run of rows; the one whose run holds `begin` finds the row
     const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
-    int64_t mine = 0;
-    for (int r = r0; r < r1; ++r) mine += line_tiles(a, row_of<HD>(a, r, ROWS));
-    int64_t inc = mine;
+    int64_t tiles = 0, units = 0, all_tiles = 0, all_units = 0, tiles_before = 0, units_before = 0;
+    if (a.B == 1) {
+      const Row r = row_of<HD>(a, 0, ROWS);
+      all_units = row_units(a, r);
+      all_tiles = all_units * r.tiles;
+    } else {
+      for (int i = r0; i < r1; ++i) {
+        const Row r = row_of<HD>(a, i, ROWS);
+        units += row_units(a, r);
+        tiles += (int64_t)row_units(a, r) * r.tiles;
+      }
+      int64_t it = tiles, iu = units;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += y;
-    }
-    if (lane == 31) s_scan[warp] = inc;
-    __syncthreads();
-    total = 0;
-    int64_t before = inc - mine;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      total += s_scan[w];
-    }
-    piece = piece_of(total, gridDim.x);
-    begin = piece * blockIdx.x;
-    if (begin >= total) return;
-    end = min(total, begin + piece);
-    if (begin >= before && begin < before + mine) {
-      for (int r = r0; r < r1; ++r) {
-        const int64_t n = line_tiles(a, row_of<HD>(a, r, ROWS));
-        if (begin < before + n) {
-          s_row = r;
-          s_at = begin - before;
-          break;
-        }
-        before += n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, iu, o);
+        if (lane >= o) { it += x; iu += y; }
+      }
+      if (lane == 31) { s_tiles[warp] = it; s_units[warp] = iu; }
+      __syncthreads();
+      tiles_before = it - tiles;
+      units_before = iu - units;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) { tiles_before += s_tiles[w]; units_before += s_units[w]; }
+        all_tiles += s_tiles[w];
+        all_units += s_units[w];
       }
     }
-    __syncthreads();
-    b = s_row;
-    off = s_at;
+    extra = all_tiles >= (int64_t)gridDim.x * 2 * kWarps ? kUnitTiles : 0;
+    total = all_tiles + extra * all_units;
+    piece = (total + gridDim.x - 1) / gridDim.x;
+    if (piece < kMinTiles) piece = kMinTiles;
+    begin = piece * blockIdx.x;
+    if (begin >= total) return;
+    end = min(total, begin + piece);
+    if (a.B == 1) {
+      off = begin;
+    } else {
+      int64_t at = tiles_before + extra * units_before;
+      if (begin >= at && begin < at + tiles + extra * units)
+        for (int i = r0; i < r1; ++i) {
+          const Row r = row_of<HD>(a, i, ROWS);
+          const int64_t n = (int64_t)row_units(a, r) * (r.tiles + extra);
+          if (begin < at + n) {
+            s_row = i;
+            s_off = begin - at;
+            break;
+          }
+          at += n;
+        }
+      __syncthreads();
+      b = s_row;
+      off = s_off;
+    }
   }
 
-  const I8Const ic = i8_const();
-  const unsigned ring = (unsigned)__cvta_generic_to_shared(sm) + warp * ST * SB;
-  unsigned char *ringp = sm + warp * ST * SB;
-  bool first = true;
-  for (int64_t left = end - begin; left > 0;) {
-    // ---- next segment
-    Row r = row_of<HD>(a, b, ROWS);
-    int64_t in_row = line_tiles(a, r);
-    while (off >= in_row) {  // rows without tiles, or the row is done
-      off -= in_row;
-      if (++b >= a.B) return;  // only if d_pos changed under the kernel
-      r = row_of<HD>(a, b, ROWS);
-      in_row = line_tiles(a, r);
-    }
-    const int unit = (int)(off / r.tiles), t0 = (int)(off - (int64_t)unit * r.tiles);
-    const int t1 = (int)min((int64_t)r.tiles, t0 + left);
-    const int g = unit / r.groups, row0 = (unit - g * r.groups) * ROWS;
-    const int64_t kvrow = (int64_t)b * c.Hkv + g;
-    const uint8_t *kc = c.codes[0] + kvrow * c.N * HD, *vc = c.codes[1] + kvrow * c.N * HD;
-    const float *ksc = c.scale[0] + kvrow * (c.N / c.block), *vsc = c.scale[1] + kvrow * (c.N / c.block);
-
-    // One tile's K (which = 0) or V rows and scales into ring slot `slot`.
-    auto issue = [&](int which, int tile, int slot) {
-      if (tile < t1) {
-        constexpr int CH = HD / 16, N = TL * CH / 32;  // 16-byte chunks of a row, copies of a lane
-        const int p0 = tile * TL, p = lane / CH, ch = lane % CH;
-        const unsigned st = ring + slot * SB + which * TL * HD;
-        const uint8_t *src = (which ? vc : kc) + (size_t)p0 * HD + lane * 16;
-        if (p0 + TL <= r.n) {
-          // copy i is 512 bytes on; at head_dim 128 the swizzle of V's rows alternates
-          const unsigned o = which ? v_off<HD>(p, ch) : k_off<HD>(p, ch), d0 = st + o;
-          const unsigned d1 = st + (which && HD == 128 ? o ^ 64 : o);
-#pragma unroll
-          for (int i = 0; i < N; ++i) cp16s((i & 1 ? d1 : d0) + i * 512, src + i * 512);
-        } else {  // the unit's last tile: zeros behind the last position
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int q = i * (32 / CH) + p, bytes = p0 + q < r.n ? 16 : 0;
-            cp16z(st + (which ? v_off<HD>(q, ch) : k_off<HD>(q, ch)), bytes ? src + i * 512 : kc, bytes);
-          }
-        }
-        if (lane < TM) {
-          const int q = p0 + lane * 16, bytes = q < r.n ? 4 : 0;
-          cp4z(ring + slot * SB + 2 * TL * HD + (which * TM + lane) * 4, (which ? vsc : ksc) + (bytes ? q / c.block : 0), bytes);
-        }
+  // ---- segments, one ahead of the one that is worked on
+  int64_t left = end - begin;
+  Row r = row_of<HD>(a, b, ROWS);
+  auto next_segment = [&](Segment &s) {
+    for (;;) {
+      if (left <= 0) return false;
+      const int64_t in_row = (int64_t)row_units(a, r) * (r.tiles + extra);
+      if (off >= in_row) {  // rows without tiles, or the row is done
+        off -= in_row;
+        if (++b >= a.B) return false;  // only if d_pos changed under the kernel
+        r = row_of<HD>(a, b, ROWS);
+        continue;
       }
-      cp_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < ST; ++i) {
-      issue(0, t0 + warp + i * kWarps, i);
-      issue(1, t0 + warp + i * kWarps, i);
+      const int unit = (int)(off / (r.tiles + extra)), rem = (int)(off - (int64_t)unit * (r.tiles + extra));
+      const int64_t u0 = end - left - rem + extra;  // where the unit's tiles begin in the line
+      const int take = (int)min((int64_t)(r.tiles + extra - rem), left);
+      s.t0 = max(0, rem - extra);
+      s.t1 = max(0, rem + take - extra);
+      off += take;
+      left -= take;
+      if (s.t1 <= s.t0) continue;
+      s.b = b;
+      s.g = unit / r.groups;
+      s.row0 = (unit - s.g * r.groups) * ROWS;
+      s.n = r.n;
+      s.count = r.count;
+      s.tiles = r.tiles;
+      s.last_piece = (int)((u0 + r.tiles - 1) / piece);
+      s.rows = (int64_t)b * c.Hkv + s.g;
+      return true;
     }
+  };
 
+  const I8Const ic = i8_const();
+  constexpr int CH = HD / 16, NC = TL * CH / 32;  // 16-byte chunks of a row, copies of a lane and tile
+  const unsigned ring = (unsigned)__cvta_generic_to_shared(sm) + warp * ST * SB;
+  const unsigned char *ringp = sm + warp * ST * SB;
+  float *so = reinterpret_cast<float *>(sm + ring_bytes(HD));
+  uint2 *sq = reinterpret_cast<uint2 *>(sm + ring_bytes(HD) + state_bytes(HD, NT));
+  const unsigned ko = k_off<HD>(lane / CH, lane % CH), vo = v_off<HD>(lane / CH, lane % CH);
+
+  // One tile's K (which = 0) or V rows and scales into ring slot `slot`.
+  auto issue = [&](int which, const Segment &s, int tile, int slot) {
+    const int p0 = tile * TL;
+    const unsigned st = ring + slot * SB + which * TL * HD;
+    const uint8_t *src = c.codes[which] + (s.rows * c.N + p0) * HD + lane * 16;
+    if (p0 + TL <= s.n) {
+      // copy i is 512 bytes on; at head_dim 128 the swizzle of V's rows alternates
+      const unsigned d0 = st + (which ? vo : ko), d1 = st + (which ? (HD == 128 ? vo ^ 64 : vo) : ko);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) cp16s((i & 1 ? d1 : d0) + i * 512, src + i * 512);
+    } else {  // the unit's last tile: zeros behind the last position
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const int q = i * (32 / CH) + lane / CH, bytes = p0 + q < s.n ? 16 : 0;
+        cp16z(st + (which ? v_off<HD>(q, lane % CH) : k_off<HD>(q, lane % CH)), bytes ? src + i * 512 : c.codes[0], bytes);
+      }
+    }
+    if (lane < TM) {
+      const int q = p0 + lane * 16, bytes = q < s.n ? 4 : 0;
+      cp4z(ring + slot * SB + 2 * TL * HD + (which * TM + lane) * 4, c.scale[which] + s.rows * (c.N / c.block) + (bytes ? q / c.block : 0), bytes);
+    }
+  };
+  // A warp's tiles run through the segments in order: index i of the current
+  // one, then the next one's.  Every step commits a K and a V group, empty if
+  // there is nothing to copy, so that waiting for all but the last 2 ST - 1
+  // groups always covers the tile at hand.
+  Segment cur, nxt;
+  if (!next_segment(cur)) return;
+  bool more = next_segment(nxt);
+  auto tiles_of = [&](const Segment &s) { return (s.t1 - s.t0 - warp + kWarps - 1) / kWarps; };  // >= 0: t1 > t0, and -3 / 4 = 0
+  int cnt = tiles_of(cur), ncnt = more ? tiles_of(nxt) : 0;
+  int filled[2] = {0, 0}, fill[2] = {0, 0}, head = 0;  // [K, V]: tiles asked for from the current segment on, and the slot of the next
+  auto step = [&](int which) {
+    const int i = filled[which];
+    if (i < cnt + ncnt) {
+      if (i < cnt) issue(which, cur, cur.t0 + warp + i * kWarps, fill[which]);
+      else issue(which, nxt, nxt.t0 + warp + (i - cnt) * kWarps, fill[which]);
+      ++filled[which];
+      fill[which] = fill[which] + 1 == ST ? 0 : fill[which] + 1;
+    }
+    cp_commit();
+  };
+  for (int i = 0; i < ST; ++i) { step(0); step(1); }
+
+  for (bool first = true;; first = false) {
     // ---- query operands: column gq of n-tile nt is query row row0 + 8 nt + gq
-    uint32_t qf[NT][KS][2];
-    float rs[NT][2];   // score factor of rows 2 tq, 2 tq + 1
+    uint32_t qf[QS ? 1 : NT][QS ? 1 : KS][2];
+    float rs[NT][2];   // score factor of rows 2 tq, 2 tq + 1 (not negative)
     float qb[NT][2];   // where their scores' sums begin
     int see[NT][2];    // positions they see
-    const int nrows = r.count * grp;
-    const float sl2 = a.scale * kLog2e;
+    const int nrows = cur.count * grp;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + 8 * nt + gq;
-      float x[HD / 4];
-      float mx = 0.f;
-      const bool ok = row < nrows;
-      const int t = row / grp, h = g * grp + row - t * grp;
-      const int64_t o = b * a.q.sb + t * a.q.st + h * a.q.sh;
+      float up, qsum = 0.f;
+      if (!QS || nt % kWarps == warp) {
+        const int row = cur.row0 + 8 * nt + gq;
+        float x[HD / 4];
+        float mx = 0.f;
+        const bool ok = row < nrows;
+        const int t = row / grp, h = cur.g * grp + row - t * grp;
+        const int64_t o = cur.b * a.q.sb + t * a.q.st + h * a.q.sh;
 #pragma unroll
-      for (int j = 0; j < HD / 64; ++j) {
+        for (int j = 0; j < HD / 64; ++j) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int64_t od = o + 64 * j + 16 * tq + 8 * v;
-          if (a.q_f32) {
-            float4 y0 = make_float4(0, 0, 0, 0), y1 = y0;
-            if (ok) {
-              y0 = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + od);
-              y1 = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + od + 4);
+          for (int v = 0; v < 2; ++v) {
+            const int64_t od = o + 64 * j + 16 * tq + 8 * v;
+            if (a.q_f32) {
+              float4 y0 = make_float4(0, 0, 0, 0), y1 = y0;
+              if (ok) {
+                y0 = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + od);
+                y1 = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + od + 4);
+              }
+              const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[16 * j + 8 * v + i] = round_act(y[i], c.act);
+            } else {
+              uint4 y = make_uint4(0, 0, 0, 0);
+              if (ok) y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + od);
+              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[16 * j + 8 * v + i] = act_to_f((uint16_t)(w[i >> 1] >> (16 * (i & 1))), c.act);
             }
-            const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[16 * j + 8 * v + i] = round_act(y[i], c.act);
-          } else {
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (ok) y = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + od);
-            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[16 * j + 8 * v + i] = act_to_f((uint16_t)(w[i >> 1] >> (16 * (i & 1))), c.act);
           }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < HD / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      int e = (int)(__float_as_uint(mx) >> 23) - 127;
-      e = min(max(e, -126), 126);
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23) * (sl2 * code_unit<FMT>());
-      float qsum = 0.f;
+        for (int i = 0; i < HD / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        int e = (int)(__float_as_uint(mx) >> 23) - 127;
+        e = min(max(e, -126), 126);
+        const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);  // the scale's sign goes to the query
+        up = __uint_as_float((uint32_t)(127 + e) << 23) * (fabsf(a.scale) * kLog2e * code_unit<FMT>());
 #pragma unroll
-      for (int j = 0; j < HD / 64; ++j)
+        for (int j = 0; j < HD / 64; ++j)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const float *y = x + 16 * j + 4 * s;
-          constexpr int E = FMT == RV_KV8_INT8 ? 2 : 1;  // the second element of unpack_k's first pair
-          qf[nt][4 * j + s][0] = pack_h2(y[0] * down, y[E] * down);
-          qf[nt][4 * j + s][1] = pack_h2(y[3 - E] * down, y[3] * down);
-          if (FMT == RV_KV8_INT8) {
-            const float2 u = __half22float2(bits_h2(qf[nt][4 * j + s][0])), v = __half22float2(bits_h2(qf[nt][4 * j + s][1]));
-            qsum += (u.x + u.y) + (v.x + v.y);
+          for (int s = 0; s < 4; ++s) {
+            const float *y = x + 16 * j + 4 * s;
+            constexpr int E = FMT == RV_KV8_INT8 ? 2 : 1;  // the second element of unpack_k's first pair
+            const uint32_t q0 = pack_h2(y[0] * down, y[E] * down), q1 = pack_h2(y[3 - E] * down, y[3] * down);
+            if (QS) sq[(nt * KS + 4 * j + s) * 32 + lane] = make_uint2(q0, q1);
+            else { qf[QS ? 0 : nt][QS ? 0 : 4 * j + s][0] = q0; qf[QS ? 0 : nt][QS ? 0 : 4 * j + s][1] = q1; }
+            if (FMT == RV_KV8_INT8) {
+              const float2 u = __half22float2(bits_h2(q0)), v = __half22float2(bits_h2(q1));
+              qsum += (u.x + u.y) + (v.x + v.y);
+            }
           }
+        if (FMT == RV_KV8_INT8) {
+          qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+          qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
         }
-      if (FMT == RV_KV8_INT8) {
-        qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
-        qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+        if (QS && tq == 0) {
+          s_rs[8 * nt + gq] = up;
+          s_qb[8 * nt + gq] = -kBias * qsum;
+        }
       }
+      if (!QS) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        rs[nt][k] = __shfl_sync(0xffffffffu, up, (2 * tq + k) * 4);
-        qb[nt][k] = -kBias * __shfl_sync(0xffffffffu, qsum, (2 * tq + k) * 4);
-        const int rr = row0 + 8 * nt + 2 * tq + k;
-        const int64_t n = (int64_t)row_pos(a.pos, b) + rr / grp + 1;
-        see[nt][k] = rr < nrows ? (int)(n < 0 ? 0 : n > r.n ? r.n : n) : r.n;  // rows that do not exist see zeros
+        for (int k = 0; k < 2; ++k) {
+          rs[nt][k] = __shfl_sync(0xffffffffu, up, (2 * tq + k) * 4);
+          qb[nt][k] = -kBias * __shfl_sync(0xffffffffu, qsum, (2 * tq + k) * 4);
+        }
       }
     }
-    int see_all = r.n;  // positions that every row of the group sees
+    if (QS) {
+      __syncthreads();
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) see_all = min(see_all, min(see[nt][0], see[nt][1]));
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          rs[nt][k] = s_rs[8 * nt + 2 * tq + k];
+          qb[nt][k] = s_qb[8 * nt + 2 * tq + k];
+        }
+    }
+    int see_all = cur.n;  // positions that every row of the group sees
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int rr = cur.row0 + 8 * nt + 2 * tq + k;
+        const int64_t n = (int64_t)row_pos(a.pos, cur.b) + rr / grp + 1;
+        see[nt][k] = rr < nrows ? (int)(n < 0 ? 0 : n > cur.n ? cur.n : n) : cur.n;  // rows that do not exist see zeros
+        see_all = min(see_all, see[nt][k]);
+      }
     see_all = __reduce_min_sync(0xffffffffu, see_all);
 
-    float o[MD][NT][4], m[NT][2], l[NT][2];
+    F2 o[MD][NT][2];  // [16-element tile][n-tile][element 2 i, 2 i + 1]: columns 2 tq, 2 tq + 1
+    float m[NT][2];
+    F2 l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt][0] = m[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
+      l[nt] = f2(0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < MD; ++i) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+      for (int i = 0; i < MD; ++i) o[i][nt][0] = o[i][nt][1] = f2(0.f, 0.f);
     }
 
-    int slot = 0;
-    for (int tile = t0 + warp; tile < t1; tile += kWarps) {
-      const unsigned char *kt = ringp + slot * SB, *vt = kt + TL * HD;
+    for (int ti = 0; ti < cnt; ++ti) {
+      const unsigned char *kt = ringp + head * SB, *vt = kt + TL * HD;
       const float *fs = reinterpret_cast<const float *>(kt + 2 * TL * HD);
-      const int p0 = tile * TL;
+      const int p0 = (cur.t0 + warp + ti * kWarps) * TL;
       cp_wait<2 * ST - 1>();
       __syncwarp();
       float s[TM][NT][4];
@@ -465,8 +545,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             unpack_k<FMT>(x1[k], f[1], f[3], ic);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              if (j == 0 && k == 0) mma16_from(s[i][nt], f, qf[nt][0][0], qf[nt][0][1], qb[nt][0], qb[nt][1]);
-              else mma16(s[i][nt], f, qf[nt][4 * j + k][0], qf[nt][4 * j + k][1]);
+              uint2 q;
+              if (QS) q = sq[(nt * KS + 4 * j + k) * 32 + lane];
+              else q = make_uint2(qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][0], qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][1]);
+              if (j == 0 && k == 0) mma16_from(s[i][nt], f, q.x, q.y, qb[nt][0], qb[nt][1]);
+              else mma16(s[i][nt], f, q.x, q.y);
             }
           }
         }
@@ -474,22 +557,14 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
       for (int i = 0; i < NG; ++i) ks[i] = fs[i * GS];
       __syncwarp();  // every lane is done with the tile's K: its slot takes the next copy
-      issue(0, tile + ST * kWarps, slot);
-      // ---- scale, mask, running maximum (column 2 tq + k of n-tile nt)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const float f = ks[i / GS] * rs[nt][k];
-            s[i][nt][k] *= f;
-            s[i][nt][2 + k] *= f;
-          }
+      step(0);
+      // ---- mask, running maximum, weights (column 2 tq + k of n-tile nt);
+      // factors are not negative, so a block's maximum is its scores' times the factor
       const bool edge = p0 + TL > see_all;
-      if (edge) {
+      uint32_t pb[TM][NT][2], pl[TM][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        if (edge) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int n = see[nt][k] - p0 - gq;
@@ -499,16 +574,19 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
               if (n <= 16 * i + 8) s[i][nt][2 + k] = -INFINITY;
             }
           }
-      }
-      uint32_t pb[TM][NT][2], pl[TM][NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float mn[2], al[2];
+        }
+        float mn[2], al[2], f[NG][2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float x = fmaxf(s[0][nt][k], s[0][nt][2 + k]);
+          float x = -INFINITY;
 #pragma unroll
-          for (int i = 1; i < TM; ++i) x = fmaxf(x, fmaxf(s[i][nt][k], s[i][nt][2 + k]));
+          for (int g = 0; g < NG; ++g) {
+            f[g][k] = ks[g] * rs[nt][k];
+            float y = fmaxf(s[g * GS][nt][k], s[g * GS][nt][2 + k]);
+#pragma unroll
+            for (int i = 1; i < GS; ++i) y = max3(y, s[g * GS + i][nt][k], s[g * GS + i][nt][2 + k]);
+            x = fmaxf(x, y * f[g][k]);  // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
+          }
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
           x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
@@ -516,44 +594,50 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           m[nt][k] = fmaxf(mo, x);
           mn[k] = m[nt][k] == -INFINITY ? 0.f : m[nt][k];
           al[k] = ex2(mo - mn[k]);
-          l[nt][k] *= al[k];
         }
+        const F2 neg = f2(-mn[0], -mn[1]), al2 = f2(al[0], al[1]);
+        l[nt] = f2_mul(l[nt], al2);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
+          const F2 ff = f2(f[i / GS][0], f[i / GS][1]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) s[i][nt][q] = ex2(s[i][nt][q] - mn[q & 1]);
-          l[nt][0] += s[i][nt][0] + s[i][nt][2];
-          l[nt][1] += s[i][nt][1] + s[i][nt][3];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t hi = pack_h2(s[i][nt][2 * k], s[i][nt][2 * k + 1]);
-            pb[i][nt][k] = transpose8(hi);
+          for (int q = 0; q < 2; ++q) {
+            float2 x = f2_split(f2_fma(f2(s[i][nt][2 * q], s[i][nt][2 * q + 1]), ff, neg));
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            if (edge) {
+              const int p = p0 + 16 * i + 8 * q + gq;
+              if (p >= see[nt][0]) x.x = 0.f;
+              if (p >= see[nt][1]) x.y = 0.f;
+            }
+            l[nt] = f2_add(l[nt], f2(x.x, x.y));
+            const uint32_t hi = pack_h2(x.x, x.y);
+            pb[i][nt][q] = transpose8(hi);
             if (LO) {
               const float2 h = __half22float2(bits_h2(hi));
-              pl[i][nt][k] = transpose8(pack_h2(s[i][nt][2 * k] - h.x, s[i][nt][2 * k + 1] - h.y));
+              pl[i][nt][q] = transpose8(pack_h2(x.x - h.x, x.y - h.y));
             }
           }
         }
         if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
           for (int i = 0; i < MD; ++i) {
-            o[i][nt][0] *= al[0]; o[i][nt][1] *= al[1]; o[i][nt][2] *= al[0]; o[i][nt][3] *= al[1];
+            o[i][nt][0] = f2_mul(o[i][nt][0], al2);
+            o[i][nt][1] = f2_mul(o[i][nt][1], al2);
           }
         }
       }
       cp_wait<2 * ST - 1>();
       __syncwarp();
-      float vs[NG][NT][2];
+      F2 vs[NG][NT];
 #pragma unroll
       for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            vs[i][nt][k] = fs[TM + i * GS] * code_unit<FMT>();
-            // a block that the row sees nothing of adds nothing, whatever its scale
-            if (edge && see[nt][k] <= p0 + 16 * GS * i) vs[i][nt][k] = 0.f;
-          }
+        for (int nt = 0; nt < NT; ++nt) {
+          const float x = fs[TM + i * GS] * code_unit<FMT>();
+          // a block that the row sees nothing of adds nothing, whatever its scale
+          vs[i][nt] = f2(edge && see[nt][0] <= p0 + 16 * GS * i ? 0.f : x, edge && see[nt][1] <= p0 + 16 * GS * i ? 0.f : x);
+        }
       float bias[NG][NT][2];  // where the products' sums begin
       if (FMT == RV_KV8_INT8) {
         const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
@@ -591,7 +675,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             }
           }
       __syncwarp();
-      issue(1, tile + ST * kWarps, slot);
+      step(1);
 #pragma unroll
       for (int wq = 0; wq < VW; ++wq) {  // a word of each V row: two 16-element tiles of O^T
         uint32_t f[TM][2][4];            // [k-step][tile][operand]
@@ -599,9 +683,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         for (int i = 0; i < TM; ++i)
 #pragma unroll
           for (int hb = 0; hb < 2; ++hb) {
-            const uint32_t w0 = vw[i][hb][0][wq], w1 = vw[i][hb][1][wq];
             uint32_t x[4];
-            unpack_v<FMT>(w0, w1, x, ic);
+            unpack_v<FMT>(vw[i][hb][0][wq], vw[i][hb][1][wq], x, ic);
             f[i][0][2 * hb] = x[0];
             f[i][0][2 * hb + 1] = x[1];
             f[i][1][2 * hb] = x[2];
@@ -611,11 +694,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float(&oo)[4] = o[2 * wq + h][nt];
+            F2(&oo)[2] = o[2 * wq + h][nt];
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
-              float acc[4];
               constexpr bool I8 = FMT == RV_KV8_INT8;
+              float acc[4];
               mma16_from(acc, f[i * GS][h], pb[i * GS][nt][0], pb[i * GS][nt][1], I8 ? bias[i][nt][0] : 0.f, I8 ? bias[i][nt][1] : 0.f);
               if (LO) mma16(acc, f[i * GS][h], pl[i * GS][nt][0], pl[i * GS][nt][1]);
 #pragma unroll
@@ -623,80 +706,92 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
                 mma16(acc, f[i * GS + j][h], pb[i * GS + j][nt][0], pb[i * GS + j][nt][1]);
                 if (LO) mma16(acc, f[i * GS + j][h], pl[i * GS + j][nt][0], pl[i * GS + j][nt][1]);
               }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) oo[q] = fmaf(acc[q], vs[i][nt][q & 1], oo[q]);
+              oo[0] = f2_fma(f2(acc[0], acc[1]), vs[i][nt], oo[0]);
+              oo[1] = f2_fma(f2(acc[2], acc[3]), vs[i][nt], oo[1]);
             }
           }
       }
-      slot = slot + 1 == ST ? 0 : slot + 1;
+      head = head + 1 == ST ? 0 : head + 1;
     }
-    cp_wait<0>();
 
     // ---- join the warps' states
+    __syncthreads();  // the states of the segment before have been read
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const float2 x = f2_split(l[nt]);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        float x = l[nt][k];
-        x += __shfl_xor_sync(0xffffffffu, x, 4);
-        x += __shfl_xor_sync(0xffffffffu, x, 8);
-        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        float y = k ? x.y : x.x;
+        y += __shfl_xor_sync(0xffffffffu, y, 4);
+        y += __shfl_xor_sync(0xffffffffu, y, 8);
+        y += __shfl_xor_sync(0xffffffffu, y, 16);
         if (gq == 0) {
           s_m[warp][8 * nt + 2 * tq + k] = m[nt][k];
-          s_l[warp][8 * nt + 2 * tq + k] = x;
+          s_l[warp][8 * nt + 2 * tq + k] = y;
         }
       }
-    __syncthreads();  // every warp is done with its ring: the states reuse it
-    float *so = reinterpret_cast<float *>(sm);
-    static_assert(kWarps * ROWS * HD * 4 <= smem_bytes(HD, NT), "the joined states fit the rings");
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float *d = so + ((warp * ROWS) + 8 * nt + 2 * tq + k) * HD + gq * (HD / 8);
-#pragma unroll
-        for (int i = 0; i < MD; i += 2)
-          *reinterpret_cast<float4 *>(d + 2 * i) = make_float4(o[i][nt][k], o[i][nt][2 + k], o[i + 1][nt][k], o[i + 1][nt][2 + k]);
-      }
-    __syncthreads();
-    const bool whole = t0 == 0 && t1 == r.tiles;
+    }
+    const bool whole = cur.t0 == 0 && cur.t1 == cur.tiles;
     float *slotp = slots + (first ? 0 : slot_floats(HD, NT));
-    if (tid == 0 && t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
-      const int64_t at = by_unit ? (int64_t)(b * c.Hkv + g) * groups + row0 / ROWS : blockIdx.x;
-      cuts[at] = Cut{b, g, row0, (int)blockIdx.x, whole ? 0 : (int)((end - left + r.tiles - 1) / piece), first ? 0 : 1, {0, 0}};
+    if (tid == 0 && cur.t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
+      const int64_t at = by_unit ? cur.rows * groups + cur.row0 / ROWS : blockIdx.x;
+      cuts[at] = Cut{cur.b, cur.g, cur.row0, (int)blockIdx.x, whole ? 0 : cur.last_piece, first ? 0 : 1, {0, 0}};
     }
-    for (int u = tid; u < ROWS * (HD / 4); u += kWarps * 32) {
-      const int rr = u / (HD / 4), d = (u - rr * (HD / 4)) * 4, row = row0 + rr;
-      if (row >= nrows) break;
-      float mm = s_m[0][rr];
+    constexpr int HV = halves(HD, NT), HE = HD / HV, HP = HD / 8 / HV;  // elements of a half; of a thread and half
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][rr]);
-      const float base = mm == -INFINITY ? 0.f : mm;
-      float ll = 0.f;
-      float4 x = make_float4(0, 0, 0, 0);
+    for (int hv = 0; hv < HV; ++hv) {
+      if (hv) __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = ex2(s_m[w][rr] - base);
-        const float4 y = *reinterpret_cast<const float4 *>(so + (w * ROWS + rr) * HD + d);
-        ll = fmaf(s_l[w][rr], f, ll);
-        x.x = fmaf(y.x, f, x.x); x.y = fmaf(y.y, f, x.y); x.z = fmaf(y.z, f, x.z); x.w = fmaf(y.w, f, x.w);
-      }
-      if (!whole) {
-        *reinterpret_cast<float4 *>(slotp + rr * HD + d) = x;
-        if (d == 0) {
-          slotp[ROWS * HD + rr] = mm;
-          slotp[ROWS * HD + ROWS + rr] = ll;
+      for (int nt = 0; nt < NT; ++nt) {
+        float *d = so + (warp * ROWS + 8 * nt + 2 * tq) * HE + gq * HP;
+#pragma unroll
+        for (int i = 0; i < MD / HV; i += 2) {
+          const float2 w0 = f2_split(o[hv * (MD / HV) + i][nt][0]), w1 = f2_split(o[hv * (MD / HV) + i][nt][1]);
+          const float2 w2 = f2_split(o[hv * (MD / HV) + i + 1][nt][0]), w3 = f2_split(o[hv * (MD / HV) + i + 1][nt][1]);
+          *reinterpret_cast<float4 *>(d + 2 * i) = make_float4(w0.x, w1.x, w2.x, w3.x);
+          *reinterpret_cast<float4 *>(d + HE + 2 * i) = make_float4(w0.y, w1.y, w2.y, w3.y);
         }
-      } else {
-        const int t = row / grp, h = g * grp + row - t * grp;
-        write_out(a, b, t, h, d, x, mm, ll);
+      }
+      __syncthreads();
+      for (int u = tid; u < ROWS * (HE / 4); u += kWarps * 32) {
+        const int rr = u / (HE / 4), e = (u - rr * (HE / 4)) * 4, d = e / HP * (HD / 8) + hv * HP + e % HP, row = cur.row0 + rr;
+        if (row >= nrows) break;
+        float mm = s_m[0][rr];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][rr]);
+        const float base = mm == -INFINITY ? 0.f : mm;
+        float ll = 0.f;
+        float4 x = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(s_m[w][rr] - base);
+          const float4 y = *reinterpret_cast<const float4 *>(so + (w * ROWS + rr) * HE + e);
+          ll = fmaf(s_l[w][rr], f, ll);
+          x.x = fmaf(y.x, f, x.x); x.y = fmaf(y.y, f, x.y); x.z = fmaf(y.z, f, x.z); x.w = fmaf(y.w, f, x.w);
+        }
+        if (!whole) {
+          *reinterpret_cast<float4 *>(slotp + rr * HD + d) = x;
+          if (d == 0) {
+            slotp[ROWS * HD + rr] = mm;
+            slotp[ROWS * HD + ROWS + rr] = ll;
+          }
+        } else {
+          const int t = row / grp, h = cur.g * grp + row - t * grp;
+          write_out(a, cur.b, t, h, d, x, mm, ll);
+        }
       }
     }
-    __syncthreads();  // the next segment's copies reuse the rings
-    first = false;
-    left -= t1 - t0;
-    off += t1 - t0;
+    if (!more) break;
+    // ---- on to the next segment, part of whose tiles are on their way
+    filled[0] -= cnt;
+    filled[1] -= cnt;
+    cur = nxt;
+    cnt = ncnt;
+    more = next_segment(nxt);
+    ncnt = more ? tiles_of(nxt) : 0;
+    for (int i = filled[0]; i < ST; ++i) { step(0); step(1); }
   }
+  cp_wait<0>();
 }
 
 // ------------------------------------------------------------------ join
