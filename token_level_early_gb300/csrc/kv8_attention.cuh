@@ -34,9 +34,6 @@
 
 #include "ops.cuh"
 
-#ifndef KUT
-#define KUT 8
-#endif
 namespace rv {
 namespace kv8a {
 
@@ -49,20 +46,26 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMinTiles = kWarps;
 // What beginning a unit costs a block, in tiles (its queries' operands, the
 // join of the warps): the line counts it, where pieces are long enough.
-constexpr int kUnitTiles = KUT;
+constexpr int kUnitTiles = 8;
 
-// Blocks per SM: as many as the registers leave room for.
+// Blocks per SM, as many as the registers leave room for; the tiles of a
+// warp's ring (K and V have their own slots: one tile still keeps a half on
+// its way while the other is worked on); query operands in shared memory or
+// in registers.  Measured for up to 8 rows, blocks / ring / operands: head_dim
+// 64, ragged batch of 64: 3/1/shared 56.8 us, 3/2/registers 59.9, 4/1/shared
+// 59.3; head_dim 128, 131K positions: 2/1/registers 50.1 us, 2/2/registers
+// 51.7, 3/1/shared 51.8, 4/1/shared 61.6 (spills).
 __host__ __device__ constexpr int blocks_per_sm(int hd, int nt) { return nt == 1 && hd == 64 ? 3 : 2; }
-constexpr int kStages = 2;  // tiles of a warp's ring
+__host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 1 : 2; }
+__host__ __device__ constexpr bool query_smem(int hd, int nt) { return nt > 1 || hd == 64; }
 // A stage: K rows, V rows, a K and a V scale for each 16 positions.
 __host__ __device__ constexpr int stage_bytes(int hd) { return 2 * tile_len(hd) * hd + 32; }
-__host__ __device__ constexpr int ring_bytes(int hd) { return kWarps * kStages * stage_bytes(hd); }
+__host__ __device__ constexpr int ring_bytes(int hd, int nt) { return kWarps * stages(nt) * stage_bytes(hd); }
 // The warps' O at a unit's end, in two halves where a whole one is too large.
 __host__ __device__ constexpr int halves(int hd, int nt) { return hd * nt > 256 ? 2 : 1; }
 __host__ __device__ constexpr int state_bytes(int hd, int nt) { return kWarps * 8 * nt * (hd / halves(hd, nt)) * 4; }
-// Query operands in shared memory (more than 8 rows; else in registers).
-__host__ __device__ constexpr int query_bytes(int hd, int nt) { return nt == 1 ? 0 : nt * (hd / 16) * 32 * 8; }
-__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd) + state_bytes(hd, nt) + query_bytes(hd, nt); }
+__host__ __device__ constexpr int query_bytes(int hd, int nt) { return query_smem(hd, nt) ? nt * (hd / 16) * 32 * 8 : 0; }
+__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd, nt) + state_bytes(hd, nt) + query_bytes(hd, nt); }
 // One cut unit's state: O [rows][hd], then m and l [rows].
 __host__ __device__ constexpr size_t slot_floats(int hd, int nt) { return (size_t)8 * nt * (hd + 2); }
 
@@ -229,7 +232,7 @@ __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, in
 struct Segment {
   int b, g, row0, t0, t1;
   int n, count, tiles;  // the row's visible positions and tokens, the unit's tiles
-  int last_piece;       // the piece that the unit ends in
+  int64_t last;         // where the unit ends in the line (its last tile)
   int64_t rows;         // KV row: b Hkv + g
 };
 
@@ -237,9 +240,9 @@ struct Segment {
 // tile).  LO: the weights enter as two fp16 terms (high and low part).
 template <int FMT, int HD, int NT, int GS, bool LO>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(const __grid_constant__ Kv8AttnArgs a, int by_unit) {
-  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = kStages, SB = stage_bytes(HD);
+  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = stages(NT), SB = stage_bytes(HD);
   constexpr int TL = tile_len(HD), TM = TL / 16, NG = TM / GS;
-  constexpr bool QS = NT > 1;  // query operands in shared memory
+  constexpr bool QS = query_smem(HD, NT);
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_rs[ROWS], s_qb[ROWS];
   __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
@@ -340,8 +343,9 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         r = row_of<HD>(a, b, ROWS);
         continue;
       }
-      const int unit = (int)(off / (r.tiles + extra)), rem = (int)(off - (int64_t)unit * (r.tiles + extra));
-      const int64_t u0 = end - left - rem + extra;  // where the unit's tiles begin in the line
+      const unsigned len = r.tiles + extra;
+      const int unit = off >> 32 ? (int)(off / len) : (int)((unsigned)off / len), rem = (int)(off - (int64_t)unit * len);
+      s.last = end - left - rem + len - 1;
       const int take = (int)min((int64_t)(r.tiles + extra - rem), left);
       s.t0 = max(0, rem - extra);
       s.t1 = max(0, rem + take - extra);
@@ -354,42 +358,20 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       s.n = r.n;
       s.count = r.count;
       s.tiles = r.tiles;
-      s.last_piece = (int)((u0 + r.tiles - 1) / piece);
       s.rows = (int64_t)b * c.Hkv + s.g;
       return true;
     }
   };
 
   const I8Const ic = i8_const();
+  const int lb = __ffs(c.block) - 1;
   constexpr int CH = HD / 16, NC = TL * CH / 32;  // 16-byte chunks of a row, copies of a lane and tile
   const unsigned ring = (unsigned)__cvta_generic_to_shared(sm) + warp * ST * SB;
   const unsigned char *ringp = sm + warp * ST * SB;
-  float *so = reinterpret_cast<float *>(sm + ring_bytes(HD));
-  uint2 *sq = reinterpret_cast<uint2 *>(sm + ring_bytes(HD) + state_bytes(HD, NT));
+  float *so = reinterpret_cast<float *>(sm + ring_bytes(HD, NT));
+  uint2 *sq = reinterpret_cast<uint2 *>(sm + ring_bytes(HD, NT) + state_bytes(HD, NT));
   const unsigned ko = k_off<HD>(lane / CH, lane % CH), vo = v_off<HD>(lane / CH, lane % CH);
 
-  // One tile's K (which = 0) or V rows and scales into ring slot `slot`.
-  auto issue = [&](int which, const Segment &s, int tile, int slot) {
-    const int p0 = tile * TL;
-    const unsigned st = ring + slot * SB + which * TL * HD;
-    const uint8_t *src = c.codes[which] + (s.rows * c.N + p0) * HD + lane * 16;
-    if (p0 + TL <= s.n) {
-      // copy i is 512 bytes on; at head_dim 128 the swizzle of V's rows alternates
-      const unsigned d0 = st + (which ? vo : ko), d1 = st + (which ? (HD == 128 ? vo ^ 64 : vo) : ko);
-#pragma unroll
-      for (int i = 0; i < NC; ++i) cp16s((i & 1 ? d1 : d0) + i * 512, src + i * 512);
-    } else {  // the unit's last tile: zeros behind the last position
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const int q = i * (32 / CH) + lane / CH, bytes = p0 + q < s.n ? 16 : 0;
-        cp16z(st + (which ? v_off<HD>(q, lane % CH) : k_off<HD>(q, lane % CH)), bytes ? src + i * 512 : c.codes[0], bytes);
-      }
-    }
-    if (lane < TM) {
-      const int q = p0 + lane * 16, bytes = q < s.n ? 4 : 0;
-      cp4z(ring + slot * SB + 2 * TL * HD + (which * TM + lane) * 4, c.scale[which] + s.rows * (c.N / c.block) + (bytes ? q / c.block : 0), bytes);
-    }
-  };
   // A warp's tiles run through the segments in order: index i of the current
   // one, then the next one's.  Every step commits a K and a V group, empty if
   // there is nothing to copy, so that waiting for all but the last 2 ST - 1
@@ -400,11 +382,31 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   auto tiles_of = [&](const Segment &s) { return (s.t1 - s.t0 - warp + kWarps - 1) / kWarps; };  // >= 0: t1 > t0, and -3 / 4 = 0
   int cnt = tiles_of(cur), ncnt = more ? tiles_of(nxt) : 0;
   int filled[2] = {0, 0}, fill[2] = {0, 0}, head = 0;  // [K, V]: tiles asked for from the current segment on, and the slot of the next
+  // Asks for the next tile's K (which = 0) or V rows and scales.
   auto step = [&](int which) {
     const int i = filled[which];
     if (i < cnt + ncnt) {
-      if (i < cnt) issue(which, cur, cur.t0 + warp + i * kWarps, fill[which]);
-      else issue(which, nxt, nxt.t0 + warp + (i - cnt) * kWarps, fill[which]);
+      const bool here = i < cnt;
+      const int p0 = ((here ? cur.t0 + i * kWarps : nxt.t0 + (i - cnt) * kWarps) + warp) * TL, n = here ? cur.n : nxt.n;
+      const int64_t rows = here ? cur.rows : nxt.rows;
+      const unsigned slot = ring + fill[which] * SB, st = slot + which * TL * HD;
+      const uint8_t *src = c.codes[which] + (rows * c.N + p0) * HD + lane * 16;
+      if (p0 + TL <= n) {
+        // copy i is 512 bytes on; at head_dim 128 the swizzle of V's rows alternates
+        const unsigned d0 = st + (which ? vo : ko), d1 = st + (which ? (HD == 128 ? vo ^ 64 : vo) : ko);
+#pragma unroll
+        for (int k = 0; k < NC; ++k) cp16s((k & 1 ? d1 : d0) + k * 512, src + k * 512);
+      } else {  // the unit's last tile: zeros behind the last position
+#pragma unroll 1
+        for (int k = 0; k < NC; ++k) {
+          const int q = k * (32 / CH) + lane / CH, bytes = p0 + q < n ? 16 : 0;
+          cp16z(st + (which ? v_off<HD>(q, lane % CH) : k_off<HD>(q, lane % CH)), bytes ? src + k * 512 : c.codes[0], bytes);
+        }
+      }
+      if (lane < TM) {
+        const int q = p0 + lane * 16, bytes = q < n ? 4 : 0;
+        cp4z(slot + 2 * TL * HD + (which * TM + lane) * 4, c.scale[which] + rows * (c.N >> lb) + (bytes ? q >> lb : 0), bytes);
+      }
       ++filled[which];
       fill[which] = fill[which] + 1 == ST ? 0 : fill[which] + 1;
     }
@@ -560,11 +562,14 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       step(0);
       // ---- mask, running maximum, weights (column 2 tq + k of n-tile nt);
       // factors are not negative, so a block's maximum is its scores' times the factor
-      const bool edge = p0 + TL > see_all;
+      // (the loop of one or no turn keeps the masks a branch: as predicated
+      // operations they would cost every tile)
+      const int edge = p0 + TL > see_all;
       uint32_t pb[TM][NT][2], pl[TM][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (edge) {
+#pragma unroll 1
+        for (int e = edge; e > 0; --e) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int n = see[nt][k] - p0 - gq;
@@ -602,23 +607,36 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           const F2 ff = f2(f[i / GS][0], f[i / GS][1]);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            float2 x = f2_split(f2_fma(f2(s[i][nt][2 * q], s[i][nt][2 * q + 1]), ff, neg));
-            x.x = ex2(x.x);
-            x.y = ex2(x.y);
-            if (edge) {
-              const int p = p0 + 16 * i + 8 * q + gq;
-              if (p >= see[nt][0]) x.x = 0.f;
-              if (p >= see[nt][1]) x.y = 0.f;
-            }
-            l[nt] = f2_add(l[nt], f2(x.x, x.y));
-            const uint32_t hi = pack_h2(x.x, x.y);
-            pb[i][nt][q] = transpose8(hi);
-            if (LO) {
-              const float2 h = __half22float2(bits_h2(hi));
-              pl[i][nt][q] = transpose8(pack_h2(x.x - h.x, x.y - h.y));
+            const float2 x = f2_split(f2_fma(f2(s[i][nt][2 * q], s[i][nt][2 * q + 1]), ff, neg));
+            s[i][nt][2 * q] = ex2(x.x);
+            s[i][nt][2 * q + 1] = ex2(x.y);
+          }
+        }
+#pragma unroll 1
+        for (int e = edge; e > 0; --e) {  // what is not seen weighs nothing, whatever its block's scale
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int n = see[nt][k] - p0 - gq;
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+              if (n <= 16 * i) s[i][nt][k] = 0.f;
+              if (n <= 16 * i + 8) s[i][nt][2 + k] = 0.f;
             }
           }
         }
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float x = s[i][nt][2 * q], y = s[i][nt][2 * q + 1];
+            l[nt] = f2_add(l[nt], f2(x, y));
+            const uint32_t hi = pack_h2(x, y);
+            pb[i][nt][q] = transpose8(hi);
+            if (LO) {
+              const float2 h = __half22float2(bits_h2(hi));
+              pl[i][nt][q] = transpose8(pack_h2(x - h.x, y - h.y));
+            }
+          }
         if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
 #pragma unroll
           for (int i = 0; i < MD; ++i) {
@@ -635,9 +653,18 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float x = fs[TM + i * GS] * code_unit<FMT>();
-          // a block that the row sees nothing of adds nothing, whatever its scale
-          vs[i][nt] = f2(edge && see[nt][0] <= p0 + 16 * GS * i ? 0.f : x, edge && see[nt][1] <= p0 + 16 * GS * i ? 0.f : x);
+          vs[i][nt] = f2(x, x);
         }
+#pragma unroll 1
+      for (int e = edge; e > 0; --e) {  // a block that a row sees nothing of adds nothing, whatever its scale
+#pragma unroll
+        for (int i = 0; i < NG; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 x = f2_split(vs[i][nt]);
+            vs[i][nt] = f2(see[nt][0] <= p0 + 16 * GS * i ? 0.f : x.x, see[nt][1] <= p0 + 16 * GS * i ? 0.f : x.y);
+          }
+      }
       float bias[NG][NT][2];  // where the products' sums begin
       if (FMT == RV_KV8_INT8) {
         const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
@@ -735,7 +762,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     float *slotp = slots + (first ? 0 : slot_floats(HD, NT));
     if (tid == 0 && cur.t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
       const int64_t at = by_unit ? cur.rows * groups + cur.row0 / ROWS : blockIdx.x;
-      cuts[at] = Cut{cur.b, cur.g, cur.row0, (int)blockIdx.x, whole ? 0 : cur.last_piece, first ? 0 : 1, {0, 0}};
+      cuts[at] = Cut{cur.b, cur.g, cur.row0, (int)blockIdx.x, whole ? 0 : (int)(cur.last / piece), first ? 0 : 1, {0, 0}};
     }
     constexpr int HV = halves(HD, NT), HE = HD / HV, HP = HD / 8 / HV;  // elements of a half; of a thread and half
 #pragma unroll
@@ -797,11 +824,14 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 // ------------------------------------------------------------------ join
 
 // Joins the states of the units that the cut of the line went through: block
-// x takes cut x of `pieces`.  WPR warps take one query row.
+// x takes cut x of `pieces`.  WPR warps take one query row, each a run of its
+// states with up to kJoin of them on their way at once: what this kernel
+// takes is the latency of its dependent loads.
+constexpr int kJoin = 6;
 template <int HD, int NT, int WPR>
 __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8AttnArgs a, int pieces) {
   constexpr int ROWS = 8 * NT, PER = HD / 32, RPB = 8 / WPR;
-  __shared__ float s_x[8][HD], s_l[8];
+  __shared__ float s_x[8][HD], s_m[8], s_l[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = a.H / a.c.Hkv;
   pdl_wait();
@@ -817,41 +847,65 @@ __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8A
 #pragma unroll
   for (int i = 0; i < PER; ++i) x[i] = 0.f;
   if (live) {
-    auto slot = [&](int c) { return work + (size_t)(2 * c + (c == c0 ? cut.slot : 0)) * slot_floats(HD, NT); };
-    for (int c = c0 + lane; c <= c1; c += 32) mm = fmaxf(mm, __ldcg(slot(c) + ROWS * HD + rr));
-    mm = warp_max(mm);
-    const float base = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-    for (int c = c0 + sub; c <= c1; c += WPR) {
-      const float *s = slot(c);
-      const float f = ex2(__ldcg(s + ROWS * HD + rr) - base);
-      ll = fmaf(__ldcg(s + ROWS * HD + ROWS + rr), f, ll);
-      float y[PER];
-      if (PER == 4) {
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + rr * HD) + lane);
-        y[0] = v.x; y[1] = v.y; y[PER - 2] = v.z; y[PER - 1] = v.w;
-      } else {
-        const float2 v = __ldcg(reinterpret_cast<const float2 *>(s + rr * HD) + lane);
-        y[0] = v.x; y[1] = v.y;
+    for (int c = c0 + sub; c <= c1; c += WPR * kJoin) {
+      float sm[kJoin], sl[kJoin], y[kJoin][PER], top = mm;
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        const int cc = c + j * WPR;
+        sm[j] = -INFINITY;
+        sl[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) y[j][i] = 0.f;
+        if (cc <= c1) {
+          const float *s = work + (size_t)(2 * cc + (cc == c0 ? cut.slot : 0)) * slot_floats(HD, NT);
+          sm[j] = __ldcg(s + ROWS * HD + rr);
+          sl[j] = __ldcg(s + ROWS * HD + ROWS + rr);
+          if (PER == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + rr * HD) + lane);
+            y[j][0] = v.x; y[j][1] = v.y; y[j][PER - 2] = v.z; y[j][PER - 1] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(s + rr * HD) + lane);
+            y[j][0] = v.x; y[j][1] = v.y;
+          }
+        }
       }
 #pragma unroll
-      for (int i = 0; i < PER; ++i) x[i] = fmaf(y[i], f, x[i]);
+      for (int j = 0; j < kJoin; ++j) top = fmaxf(top, sm[j]);
+      const float base = top == -INFINITY ? 0.f : top, old = ex2(mm - base);
+      ll *= old;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) x[i] *= old;
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        const float f = ex2(sm[j] - base);
+        ll = fmaf(sl[j], f, ll);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) x[i] = fmaf(y[j][i], f, x[i]);
+      }
+      mm = top;
     }
   }
   // through shared memory: the warps of a row, and 4 elements to a thread
 #pragma unroll
   for (int i = 0; i < PER; ++i) s_x[warp][lane * PER + i] = x[i];
-  if (lane == 0) s_l[warp] = ll;
+  if (lane == 0) {
+    s_m[warp] = mm;
+    s_l[warp] = ll;
+  }
   if (WPR > 1) __syncthreads();
   else __syncwarp();
   if (!live || sub || lane >= HD / 4) return;
+#pragma unroll
+  for (int w = 1; w < WPR; ++w) mm = fmaxf(mm, s_m[warp + w]);
+  const float base = mm == -INFINITY ? 0.f : mm;
   float4 v = make_float4(0, 0, 0, 0);
   ll = 0.f;
 #pragma unroll
   for (int w = 0; w < WPR; ++w) {
     const float4 y = *reinterpret_cast<const float4 *>(&s_x[warp + w][4 * lane]);
-    v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
-    ll += s_l[warp + w];
+    const float f = ex2(s_m[warp + w] - base);
+    v.x = fmaf(y.x, f, v.x); v.y = fmaf(y.y, f, v.y); v.z = fmaf(y.z, f, v.z); v.w = fmaf(y.w, f, v.w);
+    ll = fmaf(s_l[warp + w], f, ll);
   }
   write_out(a, b, t, h, 4 * lane, v, mm, ll);
 }
