@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   constexpr bool QS = query_smem(HD, NT);
   extern __shared__ __align__(128) unsigned char sm[];
   __shared__ float s_m[kWarps][ROWS], s_l[kWarps][ROWS], s_rs[ROWS], s_qb[ROWS];
+  __shared__ int s_see[ROWS];
   __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
   __shared__ int s_row;
   pdl_wait();
@@ -417,9 +418,17 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   for (bool first = true;; first = false) {
     // ---- query operands: column gq of n-tile nt is query row row0 + 8 nt + gq
     uint32_t qf[QS ? 1 : NT][QS ? 1 : KS][2];
-    float rs[NT][2];   // score factor of rows 2 tq, 2 tq + 1 (not negative)
-    float qb[NT][2];   // where their scores' sums begin
-    int see[NT][2];    // positions they see
+    // of rows 2 tq, 2 tq + 1: score factor (not negative), where their scores'
+    // sums begin, positions they see; with QS in shared memory too
+    float rs_[QS ? 1 : NT][2], qb_[QS ? 1 : NT][2];
+    int see_[QS ? 1 : NT][2];
+    auto rs = [&](int nt) { return QS ? *reinterpret_cast<const float2 *>(s_rs + 8 * nt + 2 * tq) : make_float2(rs_[QS ? 0 : nt][0], rs_[QS ? 0 : nt][1]); };
+    auto qb = [&](int nt) { return QS ? *reinterpret_cast<const float2 *>(s_qb + 8 * nt + 2 * tq) : make_float2(qb_[QS ? 0 : nt][0], qb_[QS ? 0 : nt][1]); };
+    auto see = [&](int nt) { return QS ? *reinterpret_cast<const int2 *>(s_see + 8 * nt + 2 * tq) : make_int2(see_[QS ? 0 : nt][0], see_[QS ? 0 : nt][1]); };
+    auto sees = [&](int row) {  // rows that do not exist see zeros
+      const int64_t n = (int64_t)row_pos(a.pos, cur.b) + row / grp + 1;
+      return row < cur.count * grp ? (int)(n < 0 ? 0 : n > cur.n ? cur.n : n) : cur.n;
+    };
     const int nrows = cur.count * grp;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -488,31 +497,22 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       if (!QS) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          rs[nt][k] = __shfl_sync(0xffffffffu, up, (2 * tq + k) * 4);
-          qb[nt][k] = -kBias * __shfl_sync(0xffffffffu, qsum, (2 * tq + k) * 4);
+          rs_[QS ? 0 : nt][k] = __shfl_sync(0xffffffffu, up, (2 * tq + k) * 4);
+          qb_[QS ? 0 : nt][k] = -kBias * __shfl_sync(0xffffffffu, qsum, (2 * tq + k) * 4);
+          see_[QS ? 0 : nt][k] = sees(cur.row0 + 8 * nt + 2 * tq + k);
         }
       }
     }
     if (QS) {
+      if (tid < ROWS) s_see[tid] = sees(cur.row0 + tid);
       __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          rs[nt][k] = s_rs[8 * nt + 2 * tq + k];
-          qb[nt][k] = s_qb[8 * nt + 2 * tq + k];
-        }
     }
     int see_all = cur.n;  // positions that every row of the group sees
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int rr = cur.row0 + 8 * nt + 2 * tq + k;
-        const int64_t n = (int64_t)row_pos(a.pos, cur.b) + rr / grp + 1;
-        see[nt][k] = rr < nrows ? (int)(n < 0 ? 0 : n > cur.n ? cur.n : n) : cur.n;  // rows that do not exist see zeros
-        see_all = min(see_all, see[nt][k]);
-      }
+    for (int nt = 0; nt < NT; ++nt) {
+      const int2 n = see(nt);
+      see_all = min(see_all, min(n.x, n.y));
+    }
     see_all = __reduce_min_sync(0xffffffffu, see_all);
 
     F2 o[MD][NT][2];  // [16-element tile][n-tile][element 2 i, 2 i + 1]: columns 2 tq, 2 tq + 1
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
               uint2 q;
               if (QS) q = sq[(nt * KS + 4 * j + k) * 32 + lane];
               else q = make_uint2(qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][0], qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][1]);
-              if (j == 0 && k == 0) mma16_from(s[i][nt], f, q.x, q.y, qb[nt][0], qb[nt][1]);
+              if (j == 0 && k == 0) mma16_from(s[i][nt], f, q.x, q.y, qb(nt).x, qb(nt).y);
               else mma16(s[i][nt], f, q.x, q.y);
             }
           }
@@ -570,9 +570,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll 1
         for (int e = edge; e > 0; --e) {
+          const int2 sn = see(nt);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int n = see[nt][k] - p0 - gq;
+            const int n = (k ? sn.y : sn.x) - p0 - gq;
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
               if (n <= 16 * i) s[i][nt][k] = -INFINITY;
@@ -581,12 +582,13 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           }
         }
         float mn[2], al[2], f[NG][2];
+        const float2 rr = rs(nt);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           float x = -INFINITY;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            f[g][k] = ks[g] * rs[nt][k];
+            f[g][k] = ks[g] * (k ? rr.y : rr.x);
             float y = fmaxf(s[g * GS][nt][k], s[g * GS][nt][2 + k]);
 #pragma unroll
             for (int i = 1; i < GS; ++i) y = max3(y, s[g * GS + i][nt][k], s[g * GS + i][nt][2 + k]);
@@ -614,9 +616,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         }
 #pragma unroll 1
         for (int e = edge; e > 0; --e) {  // what is not seen weighs nothing, whatever its block's scale
+          const int2 sn = see(nt);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const int n = see[nt][k] - p0 - gq;
+            const int n = (k ? sn.y : sn.x) - p0 - gq;
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
               if (n <= 16 * i) s[i][nt][k] = 0.f;
@@ -662,7 +665,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 x = f2_split(vs[i][nt]);
-            vs[i][nt] = f2(see[nt][0] <= p0 + 16 * GS * i ? 0.f : x.x, see[nt][1] <= p0 + 16 * GS * i ? 0.f : x.y);
+            const int2 sn = see(nt);
+            vs[i][nt] = f2(sn.x <= p0 + 16 * GS * i ? 0.f : x.x, sn.y <= p0 + 16 * GS * i ? 0.f : x.y);
           }
       }
       float bias[NG][NT][2];  // where the products' sums begin
@@ -684,8 +688,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           }
       }
       // ---- O^T += vs (V^T P^T)
-      constexpr int VW = HD / 32;  // words of a V row that a thread takes
-      uint32_t vw[TM][2][2][VW];   // [k-step][8 positions][position][word]
+      // (words of a V row that a thread takes: all at once, or where registers
+      // are short a pair at a time)
+      constexpr int VP = HD == 128 && NT == 3 ? 2 : 1, VW = HD / 32 / VP;
+#pragma unroll
+      for (int vp = 0; vp < VP; ++vp) {
+      uint32_t vw[TM][2][2][VW];  // [k-step][8 positions][position][word]
 #pragma unroll
       for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -693,16 +701,19 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int p = 16 * i + 8 * hb + 2 * tq + k;
-            if (HD == 128) {
-              const uint4 w = *reinterpret_cast<const uint4 *>(vt + v_off<HD>(p, gq));
+            const unsigned char *row = HD == 128 ? vt + v_off<HD>(p, gq) + 8 * vp : vt + v_off<HD>(p, gq >> 1) + 8 * (gq & 1);
+            if (VW == 4) {
+              const uint4 w = *reinterpret_cast<const uint4 *>(row);
               vw[i][hb][k][0] = w.x; vw[i][hb][k][1] = w.y; vw[i][hb][k][VW - 2] = w.z; vw[i][hb][k][VW - 1] = w.w;
             } else {
-              const uint2 w = *reinterpret_cast<const uint2 *>(vt + v_off<HD>(p, gq >> 1) + 8 * (gq & 1));
+              const uint2 w = *reinterpret_cast<const uint2 *>(row);
               vw[i][hb][k][0] = w.x; vw[i][hb][k][1] = w.y;
             }
           }
-      __syncwarp();
-      step(1);
+      if (vp == VP - 1) {
+        __syncwarp();
+        step(1);
+      }
 #pragma unroll
       for (int wq = 0; wq < VW; ++wq) {  // a word of each V row: two 16-element tiles of O^T
         uint32_t f[TM][2][4];            // [k-step][tile][operand]
@@ -721,7 +732,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            F2(&oo)[2] = o[2 * wq + h][nt];
+            F2(&oo)[2] = o[2 * (vp * VW + wq) + h][nt];
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
               constexpr bool I8 = FMT == RV_KV8_INT8;
@@ -737,6 +748,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
               oo[1] = f2_fma(f2(acc[2], acc[3]), vs[i][nt], oo[1]);
             }
           }
+      }
       }
       head = head + 1 == ST ? 0 : head + 1;
     }
