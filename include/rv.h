@@ -181,6 +181,22 @@ int rv_debug_dump(rv_model *m, int what, void *dst, size_t bytes);
  * advancing the cached positions.  A limit of a few microseconds makes
  * waits run out on purpose (a test of that path). */
 #define RV_OPT_WAIT_LIMIT_US 2
+/* RV_OPT_KV_CACHE: how the model keeps its K/V.  RV_KV_16BIT (default), or
+ * 8 bits with one scale for each 64 positions and KV head, int8 or e4m3 (the
+ * rv_kv8 cache below, block 64): about half the memory and half the bytes that
+ * the decode attention reads.  Decode steps quantise their K/V as they are
+ * written and attend over the 8-bit cache; a prefill attends over its own
+ * 16-bit K/V and then quantises them.  Setting it to another value forgets
+ * every cached position (as rv_kv_reset does) and replaces the cache; the new
+ * one is allocated before the old one is freed, and where that fails
+ * (RV_ENOMEM) nothing changes.  The 8-bit caches run on the chain engine
+ * (RV_ESTATE with the persistent one, either way round) and need rope_theta
+ * above 1.  RV_DUMP_KV then gives the cache's values rounded to act_dtype,
+ * and the sentinel at positions that are not cached. */
+#define RV_OPT_KV_CACHE 3
+#define RV_KV_16BIT 0
+#define RV_KV_INT8 1
+#define RV_KV_E4M3 2
 int rv_set_option(rv_model *m, int option, int value);
 
 /* Test hook: make a device allocation of this library fail.  after >= 0:
@@ -438,11 +454,20 @@ int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv_heads *out
  * arguments are bad.  Enough for every smaller B and T. */
 size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads);
 
+/* Rotary frequencies of a loaded model for contexts longer than its own
+ * (rv_rope_config above): cfg's head_dim must be the model's, rotary_dim the
+ * whole head and the layout RV_ROPE_HALF (RV_EINVAL otherwise).  NULL: back to
+ * the plain frequencies of rope_theta.  Forgets every cached position, whose
+ * keys were turned by the old ones.  Prefill, decode steps and the persistent
+ * engine all follow. */
+int rv_set_rope(rv_model *m, const rv_rope_config *cfg);
+
 /* Sizes, for callers that allocate dump buffers.  rv_param_bytes: which = 0,
  * the 16-bit parameters resident on the device (embedding, LM head, norms,
  * backbone layers 1..keep_layers); which = 1, the river (codes and
  * (scale, zero) words). */
-size_t rv_kv_bytes(const rv_model *m);
+size_t rv_kv_bytes(const rv_model *m); /* of RV_DUMP_KV */
+size_t rv_kv_cache_bytes(const rv_model *m); /* of the cache on the device (differs for the 8-bit caches) */
 size_t rv_param_bytes(const rv_model *m, int which);
 
 /* Free everything the model owns. */

@@ -192,3 +192,12 @@ def test_plain_forms():
         y = rope(x, [[5, 6, 7]], f, 8, inter)
         assert np.allclose(np.linalg.norm(y, axis=-1), np.linalg.norm(x, axis=-1))
         assert np.allclose(rope(y, [[5, 6, 7]], f, 8, inter, inverse=True), x)
+
+
+def test_model_calls_reject_a_null_handle():
+    import ctypes as C
+
+    lib = rv.lib()
+    assert lib.rv_set_rope(None, C.byref(rv.RopeConfig())) == rv.RV_EINVAL
+    assert lib.rv_set_option(None, rv.OPT_KV_CACHE, rv.KV_INT8) == rv.RV_EINVAL
+    assert lib.rv_kv_cache_bytes(None) == 0

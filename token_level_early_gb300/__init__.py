@@ -31,10 +31,12 @@ EXPORTED = ("rv_last_error", "rv_load_model", "rv_quantize_river", "rv_export_ri
             "rv_decode_step", "rv_decode_step_dev", "rv_sync_status", "rv_kv_reset", "rv_set_debug",
             "rv_debug_dump", "rv_kv_bytes", "rv_param_bytes", "rv_free_model", "rv_time_kernel", "rv_greedy_head_noalloc", "rv_offload_backbone",
             "rv_set_option", "rv_debug_fail_alloc", "rv_decode_attention_plan",
-            "rv_rope_init", "rv_rope", "rv_kv8_append", "rv_kv8_read", "rv_kv8_attention", "rv_kv8_attention_workspace")
+            "rv_rope_init", "rv_rope", "rv_kv8_append", "rv_kv8_read", "rv_kv8_attention", "rv_kv8_attention_workspace",
+            "rv_set_rope", "rv_kv_cache_bytes")
 OPT_DECODE_ENGINE, ENGINE_CHAIN, ENGINE_PERSISTENT = 0, 0, 1
 OPT_QUANTIZER, QUANT_RTN, QUANT_HQQ = 1, 0, 1
 OPT_WAIT_LIMIT_US = 2
+OPT_KV_CACHE, KV_16BIT, KV_INT8, KV_E4M3 = 3, 0, 1, 2
 F16, BF16, F32 = 0, 1, 2
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BANDS, ROPE_RAMP = range(5)
@@ -170,6 +172,8 @@ def lib():
         "rv_kv8_read": ([kp, hp, hp, i32, i32, vp, vp, vp, vp], i32),
         "rv_kv8_attention": ([kp, hp, hp, i32, i32, f32, vp, vp, vp, vp, sz, vp], i32),
         "rv_kv8_attention_workspace": ([kp, i32, i32, i32], sz),
+        "rv_set_rope": ([vp, ctypes.POINTER(RopeConfig)], i32),
+        "rv_kv_cache_bytes": ([vp], sz),
     })
     for name, (args, res) in sig.items():
         f = getattr(L, name)
@@ -367,6 +371,14 @@ class Model:
         """River quantizer of the next quantize_river: QUANT_RTN or QUANT_HQQ."""
         self.set_option(OPT_QUANTIZER, method)
 
+    def set_kv_cache(self, kind: int):
+        """KV_16BIT, KV_INT8 or KV_E4M3; forgets every cached position."""
+        self.set_option(OPT_KV_CACHE, kind)
+
+    def set_rope(self, config: Optional[RopeConfig]):
+        """Rotary frequencies for long contexts (None: the model's own); forgets every cached position."""
+        _check(lib().rv_set_rope(self._h, None if config is None else ctypes.byref(config)))
+
     def set_debug(self, enable: bool):
         _check(lib().rv_set_debug(self._h, 1 if enable else 0))
 
@@ -397,6 +409,10 @@ class Model:
 
     def kv_bytes(self) -> int:
         return int(lib().rv_kv_bytes(self._h))
+
+    def kv_cache_bytes(self) -> int:
+        """Device bytes of the K/V cache (kv_bytes: of its dump)."""
+        return int(lib().rv_kv_cache_bytes(self._h))
 
     def offload_backbone(self, keep_layers: int) -> None:
         """Free backbone layers keep_layers+1..L on the device; exits are capped at keep_layers."""

@@ -22,6 +22,7 @@
 #include "common.cuh"
 #include "gemv_core.cuh"
 #include "kernels.cuh"
+#include "ops.cuh"
 #include "stream.cuh"
 
 using namespace rv;
@@ -88,8 +89,18 @@ struct rv_model {
   std::vector<void *> river_allocs;
 
   KVGeom kv{};
-  size_t kv_bytes = 0;
+  size_t kv_bytes = 0;  // of the 16-bit cache, and of its dump
   float2 *rope_cs = nullptr;
+  rv_rope_plan rope{};  // the same frequencies for the 8-bit cache's batched steps
+
+  // 8-bit K/V cache (kv_mode RV_KV_INT8, RV_KV_E4M3): all layers, and one
+  // step's 16-bit K/V on their way into it
+  int kv_mode = RV_KV_16BIT;
+  Kv8 kv8{};             // layer 0
+  std::vector<void *> kv8_allocs;
+  size_t kv8_bytes = 0;
+  KVGeom kv_step{};      // batch 1
+  void *kv8_work = nullptr;
 
   // device state block (int32 words), see state_layout()
   int32_t *d_state = nullptr;
@@ -114,6 +125,7 @@ struct rv_model {
   float *gH = nullptr, *gHin = nullptr, *gX = nullptr, *gY = nullptr, *gY2 = nullptr, *gQ = nullptr, *gO = nullptr;
   int32_t *gLists = nullptr, *gTokens = nullptr;
   float *gHf = nullptr, *gXf = nullptr, *gLogits = nullptr;
+  uint16_t *gKV = nullptr;  // a prefill's K/V of one layer on their way into the 8-bit cache
   uint16_t *gXb = nullptr;  // 16-bit staging of GEMM rows for the tensor-core path
   uint16_t *gWhi = nullptr, *gWlo = nullptr;  // a river matrix split into 16-bit hi + lo (tensor-core rows path)
   bool tc_gemm = false;     // tcgen05 rows GEMM usable on this device
@@ -252,6 +264,58 @@ int attn_plan(const rv_model *m, int B, AttnArgs *at) {
   return gm;
 }
 
+// The plan of the model's own frequencies; without one (rope_theta <= 1)
+// rotary_dim stays 0 and the 8-bit caches are not offered.
+void plain_rope(rv_model *m) {
+  rv_rope_config rc{};
+  rc.head_dim = rc.rotary_dim = m->hd;
+  rc.layout = RV_ROPE_HALF;
+  rc.scaling = RV_ROPE_PLAIN;
+  rc.theta = (double)m->c.rope_theta;
+  m->rope = rv_rope_plan{};
+  if (rv_rope_init(&rc, &m->rope) != RV_OK) g_err.clear();
+}
+
+// -------------------------------------------------------------- 8-bit K/V cache
+
+constexpr int kKv8Block = 64;
+
+// Layer l of the 8-bit cache.
+Kv8 kv8_layer(const rv_model *m, int l) {
+  Kv8 c = m->kv8;
+  const size_t rows = (size_t)l * c.B * c.Hkv;
+  for (int i = 0; i < 2; ++i) {
+    c.codes[i] += rows * c.N * c.hd;
+    c.scale[i] += rows * (c.N / c.block);
+    c.tail[i] += rows * 2 * c.block * c.hd;
+  }
+  return c;
+}
+
+// K/V of B x T tokens from a 16-bit staging area, positions from `pos` on.
+cudaError_t kv8_append_staged(const rv_model *m, int l, const KVGeom &g, int B, int T, const int32_t *pos, cudaStream_t s) {
+  const int64_t sh = (int64_t)g.T * g.hd, sb = sh * g.Hkv;
+  Kv8Io io{Heads{g.base + g.idx(0, 0, 0, 0, 0), sb, g.hd, sh}, Heads{g.base + g.idx(0, 1, 0, 0, 0), sb, g.hd, sh}, B, T, pos, nullptr, nullptr};
+  return launch_kv8_append(kv8_layer(m, l), io, m->act, s, 1);
+}
+
+// One token per row: q and o are fp32 rows of act16-rounded values.
+cudaError_t kv8_attend(const rv_model *m, int l, const float *q, float *o, int B, const int32_t *pos, cudaStream_t s, int pdl) {
+  Kv8AttnArgs a{};
+  const int64_t row = (int64_t)m->H * m->hd;
+  a.c = kv8_layer(m, l);
+  a.q = Heads{const_cast<float *>(q), row, row, m->hd};
+  a.out = Heads{o, row, row, m->hd};
+  a.H = m->H; a.B = B; a.T = 1;
+  a.q_f32 = 1;
+  a.out_dtype = RV_F32;
+  a.round_out = 1;
+  a.scale = 1.0f / sqrtf((float)m->hd);
+  a.pos = pos;
+  a.work = m->kv8_work;
+  return launch_kv8_attention(a, m->n_sm, s, pdl);
+}
+
 // -------------------------------------------------------------- batch-1 step
 
 int enqueue_step_b1(rv_model *m, cudaStream_t s) {
@@ -265,8 +329,8 @@ int enqueue_step_b1(rv_model *m, cudaStream_t s) {
     float *hin = m->hbuf[l & 1], *hout = m->hbuf[(l + 1) & 1];
     GemvArgs a{};
     a.st = m->st;
-    a.kv = m->kv;
-    a.layer = l;
+    a.kv = m->kv_mode ? m->kv_step : m->kv;
+    a.layer = m->kv_mode ? 0 : l;
     a.L = L; a.H = m->H; a.Hkv = m->Hkv; a.hd = m->hd;
     a.eps = m->c.rms_eps;
     a.rope_cs = m->rope_cs;
@@ -286,12 +350,17 @@ int enqueue_step_b1(rv_model *m, cudaStream_t s) {
     a.decide_layer1 = 0;
     a.dbg_s = nullptr;
 
-    AttnArgs at{};
-    at.kv = m->kv; at.layer = l; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = m->act;
-    at.q = m->qbuf; at.o = m->obuf; at.len = m->st.len;
-    at.part = m->attn_part; at.counter = m->attn_counter;
-    attn_plan(m, 1, &at);
-    RV_CK(launch_attn_decode(at, 1, s, 1));
+    if (m->kv_mode) {
+      RV_CK(kv8_append_staged(m, l, m->kv_step, 1, 1, m->st.len, s));
+      RV_CK(kv8_attend(m, l, m->qbuf, m->obuf, 1, m->st.len, s, 1));
+    } else {
+      AttnArgs at{};
+      at.kv = m->kv; at.layer = l; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = m->act;
+      at.q = m->qbuf; at.o = m->obuf; at.len = m->st.len;
+      at.part = m->attn_part; at.counter = m->attn_counter;
+      attn_plan(m, 1, &at);
+      RV_CK(launch_attn_decode(at, 1, s, 1));
+    }
 
     // O projection + residual
     a.m = make_mat(m, ly, MAT_O);
@@ -386,6 +455,8 @@ int ensure_ws(rv_model *m, long rows) {
     RV_ALLOC(L, m->gWhi, sizeof(uint16_t) * wmax);
     RV_ALLOC(L, m->gWlo, sizeof(uint16_t) * wmax);
   }
+  m->gKV = nullptr;
+  if (m->kv_mode) RV_ALLOC(L, m->gKV, sizeof(uint16_t) * 2 * rows * m->kvd);
   RV_ALLOC(L, m->gY, sizeof(float) * rows * yw);
   RV_ALLOC(L, m->gY2, sizeof(float) * rows * d);
   RV_ALLOC(L, m->gQ, sizeof(float) * rows * qd);
@@ -411,23 +482,44 @@ int enqueue_layer_rows(rv_model *m, int l, int B, int T, const int32_t *base, cu
   RV_CK(launch_rmsnorm_rows(m->gH, ly.attn_norm, d, m->c.rms_eps, act, m->gX, nullptr, m->d_nrows, (int)M, s));
   for (int p = 0; p < npath; ++p)
     if (p == 1 || ly.w[MAT_QKV]) RV_CK(gemm_rows(m, make_mat(m, ly, MAT_QKV), p, m->gX, m->gY, lists[p], cnt[p], (int)M, s));
-  RopeRowsArgs ra{};
-  ra.kv = m->kv; ra.layer = l; ra.H = m->H; ra.Hkv = m->Hkv; ra.hd = m->hd; ra.act = act;
-  ra.Y = m->gY; ra.q = m->gQ; ra.rope_cs = m->rope_cs; ra.list = nullptr; ra.count = m->d_nrows;
-  ra.tokens_per_row = T; ra.base = base;
-  RV_CK(launch_rope_rows(ra, (int)M, s));
-  if (T == 1) {
-    AttnArgs at{};
-    at.kv = m->kv; at.layer = l; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = act;
-    at.q = m->gQ; at.o = m->gO; at.len = base;
-    at.part = m->attn_part; at.counter = m->attn_counter;
-    attn_plan(m, B, &at);
-    RV_CK(launch_attn_decode(at, B, s, 1));
+  if (m->kv_mode && T == 1) {
+    // one token per row: q and k turned as they stand in Y, K/V quantised from
+    // there, attention over the 8-bit cache
+    const int64_t ld = m->qkv_n, hd = m->hd;
+    RopeArgs ra{};
+    ra.in[0] = Heads{m->gY, ld, ld, hd};
+    ra.out[0] = Heads{m->gQ, (int64_t)m->qd, (int64_t)m->qd, hd};
+    ra.in[1] = ra.out[1] = Heads{m->gY + m->qd, ld, ld, hd};
+    ra.H[0] = m->H; ra.H[1] = m->Hkv;
+    ra.B = B; ra.T = 1;
+    ra.pos = base;
+    RV_CK(launch_rope(m->rope, ra, RV_F32, RV_F32, s, 1));
+    Kv8Io io{Heads{m->gY + m->qd, ld, ld, hd}, Heads{m->gY + m->qd + m->kvd, ld, ld, hd}, B, 1, base, nullptr, nullptr};
+    RV_CK(launch_kv8_append(kv8_layer(m, l), io, RV_F32, s, 1));
+    RV_CK(kv8_attend(m, l, m->gQ, m->gO, B, base, s, 1));
   } else {
-    AttnRowsArgs ar{};
-    ar.kv = m->kv; ar.layer = l; ar.H = m->H; ar.Hkv = m->Hkv; ar.hd = m->hd; ar.act = act;
-    ar.q = m->gQ; ar.o = m->gO; ar.tokens_per_row = T; ar.base = base;
-    RV_CK(launch_attn_rows(ar, (int)M, s));
+    // the cache, or a staging area of this layer's K/V that is quantised after use
+    const KVGeom kv = m->kv_mode ? KVGeom{m->gKV, B, m->Hkv, T, m->hd, 0} : m->kv;
+    const int kl = m->kv_mode ? 0 : l;
+    RopeRowsArgs ra{};
+    ra.kv = kv; ra.layer = kl; ra.H = m->H; ra.Hkv = m->Hkv; ra.hd = m->hd; ra.act = act;
+    ra.Y = m->gY; ra.q = m->gQ; ra.rope_cs = m->rope_cs; ra.list = nullptr; ra.count = m->d_nrows;
+    ra.tokens_per_row = T; ra.base = base;
+    RV_CK(launch_rope_rows(ra, (int)M, s));
+    if (T == 1) {
+      AttnArgs at{};
+      at.kv = kv; at.layer = kl; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = act;
+      at.q = m->gQ; at.o = m->gO; at.len = base;
+      at.part = m->attn_part; at.counter = m->attn_counter;
+      attn_plan(m, B, &at);
+      RV_CK(launch_attn_decode(at, B, s, 1));
+    } else {
+      AttnRowsArgs ar{};
+      ar.kv = kv; ar.layer = kl; ar.H = m->H; ar.Hkv = m->Hkv; ar.hd = m->hd; ar.act = act;
+      ar.q = m->gQ; ar.o = m->gO; ar.tokens_per_row = T; ar.base = base;
+      RV_CK(launch_attn_rows(ar, (int)M, s));
+    }
+    if (m->kv_mode) RV_CK(kv8_append_staged(m, l, kv, B, T, base, s));
   }
   for (int p = 0; p < npath; ++p)
     if (p == 1 || ly.w[MAT_O]) RV_CK(gemm_rows(m, make_mat(m, ly, MAT_O), p, m->gO, m->gY2, lists[p], cnt[p], (int)M, s));
@@ -486,6 +578,7 @@ int enqueue_step_rows(rv_model *m, int B, cudaStream_t s) {
 // the attention's K/V tiles).
 int build_stream(rv_model *m) {
   m->stream_ready = false;
+  if (m->kv_mode) return RV_OK;  // it reads the 16-bit cache: the kernel chain serves
   const int grp = m->H / m->Hkv;
   if (!stream_supported(m->hd, grp, m->act, m->has_river ? m->group : 0)) return RV_OK;
   std::vector<LayerDesc> h(m->L);
@@ -568,7 +661,7 @@ int launch_step(rv_model *m, int B) {
     RV_CK(stream_launch(m->sargs, m->stream_grid, m->stream));
     return RV_OK;
   }
-  const int key = 2 * B + attn_plan(m, B, nullptr);
+  const int key = 2 * B + (m->kv_mode ? 0 : attn_plan(m, B, nullptr));
   auto it = m->graphs.find(key);
   if (it == m->graphs.end()) {
     if (B > 1) {
@@ -635,6 +728,7 @@ void rv_free_model(rv_model *m) {
   drop_graphs(m);
   free_list(m->ws_allocs);
   free_list(m->river_allocs);
+  free_list(m->kv8_allocs);
   free_list(m->allocs);
   if (m->pinned) cudaFreeHost(m->pinned);
   if (m->own_stream && m->stream) cudaStreamDestroy(m->stream);
@@ -700,6 +794,7 @@ static int load_impl(rv_model *m, const rv_config *cfg, const void *const *weigh
   RV_CK(launch_fill_u16(m->kv.base, m->kv_bytes / 2, KV_SENTINEL, m->stream));
   RV_ALLOC(A, m->rope_cs, sizeof(float2) * (size_t)m->Tmax * (m->hd / 2));
   RV_CK(launch_rope_table(m->rope_cs, m->Tmax, m->hd, (double)c.rope_theta, m->stream));
+  plain_rope(m);
   // step state
   RV_ALLOC(A, m->d_state, sizeof(int32_t) * state_words(m->Bmax));
   RV_CK(cudaMemsetAsync(m->d_state, 0, sizeof(int32_t) * state_words(m->Bmax), m->stream));
@@ -1028,7 +1123,9 @@ int rv_kv_reset(rv_model *m, const int32_t *rows, int n_rows) {
     if (b < 0 || b >= m->Bmax) return fail(RV_EINVAL, "row %d out of range", b);
   }
   RV_CK(cudaStreamSynchronize(m->stream));
-  if (!rows) {
+  if (m->kv_mode) {
+    // positions that are not cached are never read: nothing to refill
+  } else if (!rows) {
     RV_CK(launch_fill_u16(m->kv.base, m->kv_bytes / 2, KV_SENTINEL, m->stream));
   } else {
     const size_t per = (size_t)m->Hkv * m->Tmax * m->hd;
@@ -1064,6 +1161,73 @@ int rv_set_debug(rv_model *m, int enable) {
   return build_stream(m);
 }
 
+// Replace the K/V cache by one of another kind; all cached positions are
+// forgotten.  The new memory is allocated first: on failure nothing changes.
+static int set_kv_mode(rv_model *m, int mode) {
+  if (mode != RV_KV_16BIT && mode != RV_KV_INT8 && mode != RV_KV_E4M3) return fail(RV_EINVAL, "unknown K/V cache %d", mode);
+  if (mode == m->kv_mode) return RV_OK;
+  if (mode && m->engine == RV_ENGINE_PERSISTENT) return fail(RV_ESTATE, "the persistent decode kernel reads the 16-bit cache");
+  if (mode && m->Hkv > 1024) return fail(RV_EINVAL, "the 8-bit caches hold up to 1024 KV heads");
+  if (mode && !m->rope.rotary_dim) return fail(RV_EINVAL, "the 8-bit caches need rope_theta above 1");
+  RV_CK(cudaStreamSynchronize(m->stream));
+  std::vector<void *> fresh;
+  Kv8 c{};
+  KVGeom step{nullptr, 1, m->Hkv, 1, m->hd, 1};
+  void *work = nullptr;
+  uint16_t *base = nullptr;
+  size_t bytes = 0;
+  auto take = [&](void **p, size_t n) {
+    bytes += n;
+    return dalloc(m, fresh, p, n);
+  };
+  int rc = RV_OK;
+  if (mode) {
+    c.B = m->Bmax; c.Hkv = m->Hkv; c.hd = m->hd; c.T = m->Tmax; c.block = kKv8Block;
+    c.N = (c.T + c.block - 1) / c.block * c.block;
+    c.fmt = mode == RV_KV_INT8 ? RV_KV8_INT8 : RV_KV8_E4M3;
+    c.act = m->act;
+    const size_t rows = (size_t)m->L * c.B * c.Hkv;
+    for (int i = 0; i < 2 && rc == RV_OK; ++i) {
+      rc = take(reinterpret_cast<void **>(&c.codes[i]), rows * c.N * c.hd);
+      if (rc == RV_OK) rc = take(reinterpret_cast<void **>(&c.scale[i]), sizeof(float) * rows * (c.N / c.block));
+      if (rc == RV_OK) rc = take(reinterpret_cast<void **>(&c.tail[i]), sizeof(uint16_t) * rows * 2 * c.block * c.hd);
+    }
+    if (rc == RV_OK) rc = dalloc(m, fresh, reinterpret_cast<void **>(&step.base), sizeof(uint16_t) * 2 * m->kvd);
+    if (rc == RV_OK) rc = dalloc(m, fresh, &work, kv8_attention_work(c, m->Bmax, 1, m->H, m->n_sm));
+  } else {
+    rc = take(reinterpret_cast<void **>(&base), m->kv_bytes);
+  }
+  if (rc != RV_OK) {
+    const std::string msg = g_err;
+    free_list(fresh);
+    g_err = msg;
+    return rc;
+  }
+  drop_graphs(m);  // captured steps hold the old cache's pointers
+  free_list(m->ws_allocs);
+  m->ws_rows = 0;
+  free_list(m->kv8_allocs);
+  if (m->kv.base) {
+    auto it = std::find(m->allocs.begin(), m->allocs.end(), static_cast<void *>(m->kv.base));
+    if (it != m->allocs.end()) m->allocs.erase(it);
+    cudaFree(m->kv.base);
+    m->kv.base = nullptr;
+  }
+  m->kv_mode = mode;
+  m->kv8 = c;
+  m->kv8_bytes = mode ? bytes : 0;
+  m->kv_step = step;
+  m->kv8_work = work;
+  if (mode) {
+    m->kv8_allocs = fresh;
+  } else {
+    m->kv.base = base;
+    m->allocs.push_back(base);
+  }
+  rc = rv_kv_reset(m, nullptr, 0);
+  return rc ? rc : build_stream(m);
+}
+
 int rv_set_option(rv_model *m, int option, int value) {
   g_err.clear();
   if (check_common(m)) return RV_EINVAL;
@@ -1079,6 +1243,7 @@ int rv_set_option(rv_model *m, int option, int value) {
     m->sargs.wait_ns = (unsigned long long)value * 1000ull;
     return RV_OK;
   }
+  if (option == RV_OPT_KV_CACHE) return set_kv_mode(m, value);
   if (option != RV_OPT_DECODE_ENGINE) return fail(RV_EINVAL, "unknown option %d", option);
   if (value != RV_ENGINE_CHAIN && value != RV_ENGINE_PERSISTENT) return fail(RV_EINVAL, "unknown engine %d", value);
   if (value == RV_ENGINE_PERSISTENT && !m->stream_ready)
@@ -1088,6 +1253,33 @@ int rv_set_option(rv_model *m, int option, int value) {
   return RV_OK;
 }
 
+// The 8-bit cache as the 16-bit one would lie: cached positions' values
+// rounded to act_dtype, the sentinel elsewhere; one layer at a time.
+static int dump_kv8(rv_model *m, void *dst, size_t bytes) {
+  if (bytes != m->kv_bytes) return fail(RV_EINVAL, "size mismatch: need %zu bytes", m->kv_bytes);
+  const size_t layer = m->kv_bytes / m->L;
+  std::vector<void *> tmp;
+  uint16_t *img = nullptr;
+  int rc = dalloc(m, tmp, reinterpret_cast<void **>(&img), layer);
+  if (rc) return rc;
+  auto run = [&]() -> int {
+    const KVGeom g{img, m->Bmax, m->Hkv, m->Tmax, m->hd, 0};
+    const int64_t sh = (int64_t)g.T * g.hd, sb = sh * g.Hkv;
+    for (int l = 0; l < m->L; ++l) {
+      RV_CK(launch_fill_u16(img, layer / 2, KV_SENTINEL, m->stream));
+      Kv8Io io{Heads{img, sb, g.hd, sh}, Heads{img + g.idx(0, 1, 0, 0, 0), sb, g.hd, sh}, m->Bmax, m->Tmax, nullptr, m->st.len, nullptr};
+      RV_CK(launch_kv8_read(kv8_layer(m, l), io, m->act, m->stream));
+      RV_CK(cudaMemcpyAsync(static_cast<char *>(dst) + l * layer, img, layer, cudaMemcpyDeviceToHost, m->stream));
+      RV_CK(cudaStreamSynchronize(m->stream));
+    }
+    return RV_OK;
+  };
+  rc = run();
+  if (rc) cudaStreamSynchronize(m->stream);
+  free_list(tmp);
+  return rc;
+}
+
 int rv_debug_dump(rv_model *m, int what, void *dst, size_t bytes) {
   g_err.clear();
   if (check_common(m)) return RV_EINVAL;
@@ -1095,6 +1287,7 @@ int rv_debug_dump(rv_model *m, int what, void *dst, size_t bytes) {
   RV_CK(cudaStreamSynchronize(m->stream));
   const void *src = nullptr;
   size_t need = 0;
+  if (what == RV_DUMP_KV && m->kv_mode) return dump_kv8(m, dst, bytes);
   switch (what) {
     case RV_DUMP_HIDDEN: src = m->dbg_h; need = sizeof(float) * (size_t)(m->L + 1) * m->Bmax * m->d; break;
     case RV_DUMP_S: src = m->dbg_s; need = sizeof(float) * (size_t)m->L * m->Bmax; break;
@@ -1127,14 +1320,17 @@ int rv_time_kernel(rv_model *m, int kind, int layer, int river, int iters, float
     at.kv = m->kv; at.layer = layer - 1; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = m->act;
     at.q = m->qbuf; at.o = m->obuf; at.len = m->st.len;
     at.part = m->attn_part; at.counter = m->attn_counter;
-    attn_plan(m, 1, &at);
+    if (!m->kv_mode) attn_plan(m, 1, &at);
+    const int n = std::min(m->h_len[0] + 1, m->Tmax);
     *bytes = 2.0 * m->Hkv * m->hd * 2.0 * (double)(m->h_len[0] + 1);
+    if (m->kv_mode) *bytes = 2.0 * m->Hkv * ((double)n * m->hd + 4.0 * ((n + kKv8Block - 1) / kKv8Block));
+    auto launch = [&]() { return m->kv_mode ? kv8_attend(m, layer - 1, m->qbuf, m->obuf, 1, m->st.len, s, 0) : launch_attn_decode(at, 1, s); };
     cudaEvent_t e0, e1;
     RV_CK(cudaEventCreate(&e0));
     RV_CK(cudaEventCreate(&e1));
-    RV_CK(launch_attn_decode(at, 1, s));  // warm launch
+    RV_CK(launch());  // warm launch
     RV_CK(cudaEventRecord(e0, s));
-    for (int i = 0; i < iters; ++i) RV_CK(launch_attn_decode(at, 1, s));
+    for (int i = 0; i < iters; ++i) RV_CK(launch());
     RV_CK(cudaEventRecord(e1, s));
     RV_CK(cudaEventSynchronize(e1));
     float ms = 0.f;
@@ -1204,6 +1400,30 @@ int rv_time_kernel(rv_model *m, int kind, int layer, int river, int iters, float
 }
 
 size_t rv_kv_bytes(const rv_model *m) { return m ? m->kv_bytes : 0; }
+
+size_t rv_kv_cache_bytes(const rv_model *m) { return !m ? 0 : m->kv_mode ? m->kv8_bytes : m->kv_bytes; }
+
+int rv_set_rope(rv_model *m, const rv_rope_config *cfg) {
+  g_err.clear();
+  if (check_common(m)) return RV_EINVAL;
+  rv_rope_plan plan{};
+  if (cfg) {
+    if (cfg->head_dim != m->hd || cfg->rotary_dim != m->hd) return fail(RV_EINVAL, "head_dim and rotary_dim must be the model's head (%d)", m->hd);
+    if (cfg->layout != RV_ROPE_HALF) return fail(RV_EINVAL, "the model's heads are in the half layout");
+    int rc = rv_rope_init(cfg, &plan);
+    if (rc) return rc;
+  }
+  RV_CK(cudaStreamSynchronize(m->stream));
+  if (cfg) {
+    RV_CK(rv::launch_rope_table(plan, m->rope_cs, m->Tmax, m->stream));
+    m->rope = plan;
+  } else {
+    RV_CK(launch_rope_table(m->rope_cs, m->Tmax, m->hd, (double)m->c.rope_theta, m->stream));
+    plain_rope(m);
+  }
+  drop_graphs(m);  // batched steps over the 8-bit cache hold the plan
+  return rv_kv_reset(m, nullptr, 0);
+}
 
 int rv_debug_fail_alloc(int after) {
   g_fail_after.store(after < 0 ? -1 : after);

@@ -138,12 +138,13 @@ struct StepState {
   int32_t *err;           // scalar error flags (bit 0 token, bit 1 forced value, bit 2 quant)
 };
 
-// KV cache geometry: [L][2][max_batch][Hkv][max_seq][hd] 16-bit.
+// KV cache geometry: [L][2][max_batch][Hkv][max_seq][hd] 16-bit.  one = 1: a
+// staging area for one step's K/V, where every position is slot 0 (T = 1).
 struct KVGeom {
   uint16_t *base;
-  int B, Hkv, T, hd;
+  int B, Hkv, T, hd, one;
   __host__ __device__ size_t idx(int l, int kv, int b, int g, int p) const {
-    return ((((size_t)l * 2 + kv) * B + b) * Hkv + g) * (size_t)T * hd + (size_t)p * hd;
+    return ((((size_t)l * 2 + kv) * B + b) * Hkv + g) * (size_t)T * hd + (size_t)(one ? 0 : p) * hd;
   }
 };
 

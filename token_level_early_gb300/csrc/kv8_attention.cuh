@@ -847,6 +847,7 @@ __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8A
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = a.H / a.c.Hkv;
   pdl_wait();
+  pdl_trigger();
   const Cut *cuts = static_cast<const Cut *>(a.work);
   const float *work = reinterpret_cast<const float *>(cuts + pieces);
   const Cut cut = cuts[blockIdx.x];

@@ -91,7 +91,7 @@ struct RopeArgs {
   const int32_t *pos, *count;
   int inverse;
 };
-cudaError_t launch_rope(const rv_rope_plan &plan, const RopeArgs &a, int in_dtype, int out_dtype, cudaStream_t s);
+cudaError_t launch_rope(const rv_rope_plan &plan, const RopeArgs &a, int in_dtype, int out_dtype, cudaStream_t s, int pdl = 0);
 // (cos, sin) of positions 0..T-1 x head_dim/2 pairs, times the attention factor.
 cudaError_t launch_rope_table(const rv_rope_plan &plan, float2 *cs, int T, cudaStream_t s);
 

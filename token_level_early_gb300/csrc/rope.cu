@@ -160,6 +160,8 @@ struct Item {
 // and store them.
 template <int IN, int OUT, bool HALF>
 __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ rv_rope_plan plan, const __grid_constant__ RopeArgs a, RopeGrid g) {
+  pdl_wait();
+  pdl_trigger();
   constexpr int kItems = IN == RV_F32 ? 2 : 4;
   extern __shared__ float2 cs[];  // [tokens_per_block][pairs]
   const int pairs = plan.rotary_dim / 2, tok0 = blockIdx.x * g.tokens_per_block;
@@ -248,7 +250,7 @@ __global__ void __launch_bounds__(kThreads) k_rope(const __grid_constant__ rv_ro
 }
 
 template <int IN, int OUT>
-cudaError_t launch_io(const rv_rope_plan &plan, const RopeArgs &a, cudaStream_t s) {
+cudaError_t launch_io(const rv_rope_plan &plan, const RopeArgs &a, cudaStream_t s, int pdl) {
   const int chunks = plan.head_dim / 16, items = (a.H[0] + a.H[1]) * chunks, pairs = plan.rotary_dim / 2, tokens = a.B * a.T;
   RopeGrid g;
   // as many tokens as the threads' first items cover, but enough blocks to fill the GPU
@@ -263,8 +265,7 @@ cudaError_t launch_io(const rv_rope_plan &plan, const RopeArgs &a, cudaStream_t 
   const int grid = (tokens + tpb - 1) / tpb;
   const size_t smem = sizeof(float2) * pairs * tpb;
   auto fn = plan.layout == RV_ROPE_HALF ? k_rope<IN, OUT, true> : k_rope<IN, OUT, false>;
-  fn<<<grid, kThreads, smem, s>>>(plan, a, g);
-  return cudaGetLastError();
+  return launch_k(fn, dim3(grid), dim3(kThreads), smem, s, pdl, plan, a, g);
 }
 
 __global__ void k_rope_plan_table(const __grid_constant__ rv_rope_plan plan, float2 *cs, int T) {
@@ -277,12 +278,12 @@ __global__ void k_rope_plan_table(const __grid_constant__ rv_rope_plan plan, flo
 
 }  // namespace
 
-cudaError_t launch_rope(const rv_rope_plan &plan, const RopeArgs &a, int in_dtype, int out_dtype, cudaStream_t s) {
+cudaError_t launch_rope(const rv_rope_plan &plan, const RopeArgs &a, int in_dtype, int out_dtype, cudaStream_t s, int pdl) {
   if (in_dtype == RV_F32) {
-    if (out_dtype == RV_F32) return launch_io<RV_F32, RV_F32>(plan, a, s);
-    return out_dtype == RV_F16 ? launch_io<RV_F32, RV_F16>(plan, a, s) : launch_io<RV_F32, RV_BF16>(plan, a, s);
+    if (out_dtype == RV_F32) return launch_io<RV_F32, RV_F32>(plan, a, s, pdl);
+    return out_dtype == RV_F16 ? launch_io<RV_F32, RV_F16>(plan, a, s, pdl) : launch_io<RV_F32, RV_BF16>(plan, a, s, pdl);
   }
-  return in_dtype == RV_F16 ? launch_io<RV_F16, RV_F16>(plan, a, s) : launch_io<RV_BF16, RV_BF16>(plan, a, s);
+  return in_dtype == RV_F16 ? launch_io<RV_F16, RV_F16>(plan, a, s, pdl) : launch_io<RV_BF16, RV_BF16>(plan, a, s, pdl);
 }
 
 cudaError_t launch_rope_table(const rv_rope_plan &plan, float2 *cs, int T, cudaStream_t s) {
