@@ -230,6 +230,8 @@ struct ReadGrid {
 };
 template <int OUT, int FMT, int HD>
 __global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
+  pdl_wait();
+  pdl_trigger();
   constexpr int CH = HD / 16;
   const int kv = blockIdx.y & 1, per = g.heads * CH, pass = blockDim.x / per, b = blockIdx.z;  // tokens of a pass
   const Heads &out = kv ? io.v : io.k;
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
 }
 
 template <int OUT, int FMT>
-cudaError_t read_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s) {
+cudaError_t read_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s, int pdl) {
   const int chunks = c.hd / 16, most = 256 / chunks;
   ReadGrid g;
   g.heads = c.Hkv < most ? c.Hkv : most;
@@ -273,8 +275,7 @@ cudaError_t read_t(const Kv8 &c, const Kv8Io &io, cudaStream_t s) {
       g.wide = false;
   const int per = g.heads * chunks, pass = 256 / per, tokens = pass * kReadItems;
   auto fn = c.hd == 64 ? k_read<OUT, FMT, 64> : k_read<OUT, FMT, 128>;
-  fn<<<dim3((io.T + tokens - 1) / tokens, 2 * g.groups, io.B), pass * per, 0, s>>>(c, io, g);
-  return cudaGetLastError();
+  return launch_k(fn, dim3((io.T + tokens - 1) / tokens, 2 * g.groups, io.B), dim3(pass * per), 0, s, pdl, c, io, g);
 }
 
 }  // namespace
@@ -305,9 +306,9 @@ cudaError_t launch_kv8_append(const Kv8 &c, const Kv8Io &io, int in_dtype, cudaS
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaStream_t s) {
+cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaStream_t s, int pdl) {
 #define RV_R(OUT_) \
-  if (out_dtype == OUT_) return c.fmt == RV_KV8_INT8 ? read_t<OUT_, RV_KV8_INT8>(c, io, s) : read_t<OUT_, RV_KV8_E4M3>(c, io, s);
+  if (out_dtype == OUT_) return c.fmt == RV_KV8_INT8 ? read_t<OUT_, RV_KV8_INT8>(c, io, s, pdl) : read_t<OUT_, RV_KV8_E4M3>(c, io, s, pdl);
   RV_R(RV_F16) RV_R(RV_BF16) RV_R(RV_F32)
 #undef RV_R
   return cudaErrorInvalidValue;
@@ -400,7 +401,7 @@ extern "C" int rv_kv8_append(const rv_kv8 *cache, const rv_heads *k, const rv_he
   if (int rc = check_index(d_pos, d_count, d_err)) return rc;
   if (int rc = check_memory(cache, k->data, v->data, d_pos, d_count, d_err)) return rc;
   Kv8Io io{heads_of(k), heads_of(v), B, T, d_pos, d_count, d_err};
-  return launched("rv_kv8_append", launch_kv8_append(kv8_of(cache), io, k->dtype, static_cast<cudaStream_t>(stream)));
+  return launched("rv_kv8_append", launch_kv8_append(kv8_of(cache), io, k->dtype, static_cast<cudaStream_t>(stream), 1));
 }
 
 extern "C" int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_out, int B, int T,
@@ -417,7 +418,7 @@ extern "C" int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_
   if (int rc = check_index(d_pos, d_count, d_err)) return rc;
   if (int rc = check_memory(cache, k_out ? k_out->data : nullptr, v_out ? v_out->data : nullptr, d_pos, d_count, d_err)) return rc;
   Kv8Io io{heads_of(k_out), heads_of(v_out), B, T, d_pos, d_count, d_err};
-  return launched("rv_kv8_read", launch_kv8_read(kv8_of(cache), io, (k_out ? k_out : v_out)->dtype, static_cast<cudaStream_t>(stream)));
+  return launched("rv_kv8_read", launch_kv8_read(kv8_of(cache), io, (k_out ? k_out : v_out)->dtype, static_cast<cudaStream_t>(stream), 1));
 }
 
 namespace {
@@ -470,5 +471,5 @@ extern "C" int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv
   a.pos = d_pos; a.count = d_count;
   a.lse = d_lse;
   a.work = workspace;
-  return launched("rv_kv8_attention", launch_kv8_attention(a, n_sm, static_cast<cudaStream_t>(stream)));
+  return launched("rv_kv8_attention", launch_kv8_attention(a, n_sm, static_cast<cudaStream_t>(stream), 1));
 }

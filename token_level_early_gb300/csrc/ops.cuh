@@ -11,6 +11,11 @@
 
 namespace rv {
 
+// Every kernel of these operators waits for its predecessor's end before it
+// touches memory (griddepcontrol.wait), so all of them may be launched with
+// programmatic dependence on whatever is before them in the stream: the
+// launch then overlaps the predecessor's tail.
+
 // Records the message and returns the code.
 int op_fail(int code, const char *fmt, ...);
 
@@ -110,7 +115,7 @@ struct Kv8Io {
   int32_t *err;
 };
 cudaError_t launch_kv8_append(const Kv8 &c, const Kv8Io &io, int in_dtype, cudaStream_t s, int pdl = 0);
-cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaStream_t s);
+cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaStream_t s, int pdl = 0);
 
 struct Kv8AttnArgs {
   Kv8 c;

@@ -392,7 +392,7 @@ extern "C" int rv_rope(const rv_rope_plan *plan, const rv_heads *q_in, const rv_
   a.B = B; a.T = T;
   a.pos = d_pos; a.count = d_count;
   a.inverse = inverse != 0;
-  const cudaError_t e = launch_rope(*plan, a, q_in->dtype, q_out->dtype, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_rope(*plan, a, q_in->dtype, q_out->dtype, static_cast<cudaStream_t>(stream), 1);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return op_fail(RV_ECUDA, "rv_rope: %s", cudaGetErrorString(e));
