@@ -532,29 +532,38 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       const int p0 = (cur.t0 + warp + ti * kWarps) * TL;
       cp_wait<2 * ST - 1>();
       __syncwarp();
+      // (products in an order that keeps those into one sum apart: an mma waits
+      // for the one before it only if it adds to its result)
       float s[TM][NT][4];
 #pragma unroll
-      for (int j = 0; j < HD / 64; ++j)
+      for (int j = 0; j < HD / 64; ++j) {
+        uint4 w[TM][2];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const uint4 w0 = *reinterpret_cast<const uint4 *>(kt + k_off<HD>(16 * i + gq, 4 * j + tq));
-          const uint4 w1 = *reinterpret_cast<const uint4 *>(kt + k_off<HD>(16 * i + gq + 8, 4 * j + tq));
-          const uint32_t x0[4] = {w0.x, w0.y, w0.z, w0.w}, x1[4] = {w1.x, w1.y, w1.z, w1.w};
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 2; ++k) w[i][k] = *reinterpret_cast<const uint4 *>(kt + k_off<HD>(16 * i + gq + 8 * k, 4 * j + tq));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint2 q[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (QS) q[nt] = sq[(nt * KS + 4 * j + k) * 32 + lane];
+            else q[nt] = make_uint2(qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][0], qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][1]);
+          }
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            const uint32_t x0[4] = {w[i][0].x, w[i][0].y, w[i][0].z, w[i][0].w}, x1[4] = {w[i][1].x, w[i][1].y, w[i][1].z, w[i][1].w};
             uint32_t f[4];
             unpack_k<FMT>(x0[k], f[0], f[2], ic);
             unpack_k<FMT>(x1[k], f[1], f[3], ic);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              uint2 q;
-              if (QS) q = sq[(nt * KS + 4 * j + k) * 32 + lane];
-              else q = make_uint2(qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][0], qf[QS ? 0 : nt][QS ? 0 : 4 * j + k][1]);
-              if (j == 0 && k == 0) mma16_from(s[i][nt], f, q.x, q.y, qb(nt).x, qb(nt).y);
-              else mma16(s[i][nt], f, q.x, q.y);
+              if (j == 0 && k == 0) mma16_from(s[i][nt], f, q[nt].x, q[nt].y, qb(nt).x, qb(nt).y);
+              else mma16(s[i][nt], f, q[nt].x, q[nt].y);
             }
           }
         }
+      }
       float ks[NG];
 #pragma unroll
       for (int i = 0; i < NG; ++i) ks[i] = fs[i * GS];
@@ -673,19 +682,26 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       if (FMT == RV_KV8_INT8) {
         const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
-        for (int i = 0; i < NG; ++i)
+        for (int i = 0; i < NG; ++i) {
+          float x[NT][4];
+#pragma unroll
+          for (int j = 0; j < GS; ++j) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (j == 0) mma16_from(x[nt], one, pb[i * GS][nt][0], pb[i * GS][nt][1], 0.f, 0.f);
+              else mma16(x[nt], one, pb[i * GS + j][nt][0], pb[i * GS + j][nt][1]);
+            }
+            if (LO) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16(x[nt], one, pl[i * GS + j][nt][0], pl[i * GS + j][nt][1]);
+            }
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float x[4];
-#pragma unroll
-            for (int j = 0; j < GS; ++j) {
-              if (j == 0) mma16_from(x, one, pb[i * GS][nt][0], pb[i * GS][nt][1], 0.f, 0.f);
-              else mma16(x, one, pb[i * GS + j][nt][0], pb[i * GS + j][nt][1]);
-              if (LO) mma16(x, one, pl[i * GS + j][nt][0], pl[i * GS + j][nt][1]);
-            }
-            bias[i][nt][0] = -kBias * x[0];
-            bias[i][nt][1] = -kBias * x[1];
+            bias[i][nt][0] = -kBias * x[nt][0];
+            bias[i][nt][1] = -kBias * x[nt][1];
           }
+        }
       }
       // ---- O^T += vs (V^T P^T)
       // (words of a V row that a thread takes: all at once, or where registers
@@ -728,25 +744,38 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             f[i][1][2 * hb] = x[2];
             f[i][1][2 * hb + 1] = x[3];
           }
+        constexpr bool I8 = FMT == RV_KV8_INT8;
+        constexpr int HH = NT == 1 ? 2 : 1;  // tiles whose sums run side by side
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h0 = 0; h0 < 2; h0 += HH)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            F2(&oo)[2] = o[2 * (vp * VW + wq) + h][nt];
+          for (int i = 0; i < NG; ++i) {
+            float acc[HH][NT][4];
 #pragma unroll
-            for (int i = 0; i < NG; ++i) {
-              constexpr bool I8 = FMT == RV_KV8_INT8;
-              float acc[4];
-              mma16_from(acc, f[i * GS][h], pb[i * GS][nt][0], pb[i * GS][nt][1], I8 ? bias[i][nt][0] : 0.f, I8 ? bias[i][nt][1] : 0.f);
-              if (LO) mma16(acc, f[i * GS][h], pl[i * GS][nt][0], pl[i * GS][nt][1]);
+            for (int j = 0; j < GS; ++j) {
+              const int st = i * GS + j;
 #pragma unroll
-              for (int j = 1; j < GS; ++j) {
-                mma16(acc, f[i * GS + j][h], pb[i * GS + j][nt][0], pb[i * GS + j][nt][1]);
-                if (LO) mma16(acc, f[i * GS + j][h], pl[i * GS + j][nt][0], pl[i * GS + j][nt][1]);
+              for (int h = 0; h < HH; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  if (j == 0) mma16_from(acc[h][nt], f[st][h0 + h], pb[st][nt][0], pb[st][nt][1], I8 ? bias[i][nt][0] : 0.f, I8 ? bias[i][nt][1] : 0.f);
+                  else mma16(acc[h][nt], f[st][h0 + h], pb[st][nt][0], pb[st][nt][1]);
+                }
+              if (LO) {
+#pragma unroll
+                for (int h = 0; h < HH; ++h)
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) mma16(acc[h][nt], f[st][h0 + h], pl[st][nt][0], pl[st][nt][1]);
               }
-              oo[0] = f2_fma(f2(acc[0], acc[1]), vs[i][nt], oo[0]);
-              oo[1] = f2_fma(f2(acc[2], acc[3]), vs[i][nt], oo[1]);
             }
+#pragma unroll
+            for (int h = 0; h < HH; ++h)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                F2(&oo)[2] = o[2 * (vp * VW + wq) + h0 + h][nt];
+                oo[0] = f2_fma(f2(acc[h][nt][0], acc[h][nt][1]), vs[i][nt], oo[0]);
+                oo[1] = f2_fma(f2(acc[h][nt][2], acc[h][nt][3]), vs[i][nt], oo[1]);
+              }
           }
       }
       }
