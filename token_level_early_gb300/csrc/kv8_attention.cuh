@@ -66,6 +66,12 @@ __host__ __device__ constexpr int halves(int hd, int nt) { return hd * nt > 256 
 __host__ __device__ constexpr int state_bytes(int hd, int nt) { return kWarps * 8 * nt * (hd / halves(hd, nt)) * 4; }
 __host__ __device__ constexpr int query_bytes(int hd, int nt) { return query_smem(hd, nt) ? nt * (hd / 16) * 32 * 8 : 0; }
 __host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd, nt) + state_bytes(hd, nt) + query_bytes(hd, nt); }
+// The reference that a row's weights are taken against, exp2(x - m), follows
+// its scores' maximum only when that is ahead by more than kLag: weights up to
+// 2^kLag are as good in fp16 and fp32, and a tile that raises no maximum needs
+// no reduction over the warp and no rescaling.  kUnseen: nothing seen yet
+// (finite, so that -m stays an ordinary addend).
+constexpr float kLag = 8.f, kUnseen = -1e30f;
 // One cut unit's state: O [rows][hd], then m and l [rows].
 __host__ __device__ constexpr size_t slot_floats(int hd, int nt) { return (size_t)8 * nt * (hd + 2); }
 
@@ -520,7 +526,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     F2 l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kUnseen;
       l[nt] = f2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < MD; ++i) o[i][nt][0] = o[i][nt][1] = f2(0.f, 0.f);
@@ -569,12 +575,14 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       for (int i = 0; i < NG; ++i) ks[i] = fs[i * GS];
       __syncwarp();  // every lane is done with the tile's K: its slot takes the next copy
       step(0);
-      // ---- mask, running maximum, weights (column 2 tq + k of n-tile nt);
-      // factors are not negative, so a block's maximum is its scores' times the factor
-      // (the loop of one or no turn keeps the masks a branch: as predicated
+      // ---- mask, reference, weights (column 2 tq + k of n-tile nt); factors
+      // are not negative, so a block's maximum is its scores' times the factor
+      // (the loops of one or no turn keep the masks a branch: as predicated
       // operations they would cost every tile)
       const int edge = p0 + TL > see_all;
       uint32_t pb[TM][NT][2], pl[TM][NT][2];
+      float top[NT][2];
+      bool ahead = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll 1
@@ -590,32 +598,51 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             }
           }
         }
-        float mn[2], al[2], f[NG][2];
         const float2 rr = rs(nt);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          float x = -INFINITY;
+          top[nt][k] = -INFINITY;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            f[g][k] = ks[g] * (k ? rr.y : rr.x);
             float y = fmaxf(s[g * GS][nt][k], s[g * GS][nt][2 + k]);
 #pragma unroll
             for (int i = 1; i < GS; ++i) y = max3(y, s[g * GS + i][nt][k], s[g * GS + i][nt][2 + k]);
-            x = fmaxf(x, y * f[g][k]);  // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
+            // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
+            top[nt][k] = fmaxf(top[nt][k], y * (ks[g] * (k ? rr.y : rr.x)));
           }
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mo = m[nt][k];
-          m[nt][k] = fmaxf(mo, x);
-          mn[k] = m[nt][k] == -INFINITY ? 0.f : m[nt][k];
-          al[k] = ex2(mo - mn[k]);
+          ahead |= top[nt][k] > m[nt][k] + kLag;
         }
-        const F2 neg = f2(-mn[0], -mn[1]), al2 = f2(al[0], al[1]);
-        l[nt] = f2_mul(l[nt], al2);
+      }
+      if (__any_sync(0xffffffffu, ahead)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float al[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float x = top[nt][k];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            x = fmaxf(x, m[nt][k]);
+            al[k] = ex2(m[nt][k] - x);
+            m[nt][k] = x;
+          }
+          const F2 al2 = f2(al[0], al[1]);
+          l[nt] = f2_mul(l[nt], al2);
+#pragma unroll
+          for (int i = 0; i < MD; ++i) {
+            o[i][nt][0] = f2_mul(o[i][nt][0], al2);
+            o[i][nt][1] = f2_mul(o[i][nt][1], al2);
+          }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 rr = rs(nt);
+        const F2 neg = f2(-m[nt][0], -m[nt][1]);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const F2 ff = f2(f[i / GS][0], f[i / GS][1]);
+          const F2 ff = f2_mul(f2(ks[i / GS], ks[i / GS]), f2(rr.x, rr.y));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float2 x = f2_split(f2_fma(f2(s[i][nt][2 * q], s[i][nt][2 * q + 1]), ff, neg));
@@ -649,13 +676,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
               pl[i][nt][q] = transpose8(pack_h2(x - h.x, y - h.y));
             }
           }
-        if (__any_sync(0xffffffffu, al[0] != 1.f || al[1] != 1.f)) {
-#pragma unroll
-          for (int i = 0; i < MD; ++i) {
-            o[i][nt][0] = f2_mul(o[i][nt][0], al2);
-            o[i][nt][1] = f2_mul(o[i][nt][1], al2);
-          }
-        }
       }
       cp_wait<2 * ST - 1>();
       __syncwarp();
@@ -794,7 +814,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         y += __shfl_xor_sync(0xffffffffu, y, 8);
         y += __shfl_xor_sync(0xffffffffu, y, 16);
         if (gq == 0) {
-          s_m[warp][8 * nt + 2 * tq + k] = m[nt][k];
+          s_m[warp][8 * nt + 2 * tq + k] = m[nt][k] == kUnseen ? -INFINITY : m[nt][k];
           s_l[warp][8 * nt + 2 * tq + k] = y;
         }
       }
