@@ -377,7 +377,8 @@ int rv_rope_init(const rv_rope_config *cfg, rv_rope_plan *plan);
  * the inputs are RV_F32 and the outputs one 16-bit type.  inverse != 0 turns
  * the other way (and scales by the same attention factor): that is the
  * gradient of the rotation, dL/dx from dL/dy.  The arithmetic is fp32, each
- * output rounded once.  Any int32 position, negative ones included. */
+ * output rounded once.  Any int32 position, negative ones included.  A token's
+ * query and key heads hold at most 2^19 elements together. */
 int rv_rope(const rv_rope_plan *plan, const rv_heads *q_in, const rv_heads *q_out, const rv_heads *k_in,
             const rv_heads *k_out, int B, int T, const int32_t *d_pos, const int32_t *d_count, int inverse,
             void *stream);

@@ -230,6 +230,22 @@ def test_append_and_read_report_positions_outside():
     assert np.array_equal(f64(got[0])[2, 2:], val8[:6]) and val.shape == (6, 1, 64)
 
 
+def test_append_at_the_caches_end_changes_nothing():
+    """A first position at or behind max_seq, in the last open block's range too."""
+    c = Cache(2, 2, 64, 20, 16, 0, 0)
+    k = data(1, 2, 20, 2, 64, 0)
+    c.append(k, k, [0, 0])
+    before = [t.clone() for t in c.codes + c.scale + c.tail]
+    for pos in (20, 21, 31, 32, 2 ** 31 - 1):
+        c.append(k[:, :3].contiguous() * 5, k[:, :3].contiguous() * 5, [pos, pos])
+        assert int(c.err) == 64
+        c.err.zero_()
+    c.append(k, k, [20, 20], [0, 0])  # no tokens: no error either
+    assert int(c.err) == 0
+    for a, b in zip(before, c.codes + c.scale + c.tail):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 @pytest.mark.parametrize("act", [0, 1])
 def test_read_rounds_once_and_saturates(act):
     c = Cache(1, 1, 64, 48, 16, 0, act)
@@ -388,6 +404,48 @@ def test_attention_large_and_small_queries():
         q = data(23, 1, 2, 3, 64, 1, False) * mul
         out, lse = c.attention(q, scale, [48])
         check_attention(c, kk, vv, q, scale, [48], None, out, lse)
+
+
+def test_attention_scores_far_from_zero():
+    """Scores around +-1e4 and rows whose maxima rise from tile to tile: the
+    reference of the weights has to follow."""
+    hd, n, block = 64, 700, 32
+    for sign in (1.0, -1.0):
+        k = torch.zeros(1, n, 1, hd)
+        k[0, :, 0, 0] = sign * torch.linspace(1.0, 200.0, n)
+        k[0, :, 0, 1:] = torch.randn(n, hd - 1, generator=torch.Generator().manual_seed(3)) * 0.1
+        v = data(31, 1, n, 1, hd, 1, False)
+        q = data(32, 1, 2, 2, hd, 1, False)
+        q[..., 0] = 50.0
+        c = Cache(1, 1, hd, n, block, 1, 1)
+        k = k.to(torch.bfloat16).cuda()
+        c.append(k, v, [0])
+        kk, vv = [expect(c, f64(k)[0], n)[0]], [expect(c, f64(v)[0], n)[0]]
+        out, lse = c.attention(q, 1.0, [n - 2])
+        check_attention(c, kk, vv, q, 1.0, [n - 2], None, out, lse)
+
+
+def test_calls_refuse_what_is_not_device_memory():
+    c = Cache(1, 2, 64, 32, 16, 0, 1)
+    x = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
+    d = x.cuda()
+    need = rv.kv8_attention_workspace(c.c, 1, 1, 2)
+    w = torch.zeros(need, dtype=torch.uint8).cuda()
+    bad = rv.KV8.from_buffer_copy(c.c)
+    host = torch.zeros(4096, dtype=torch.uint8)
+    bad.k_scale = (host.data_ptr() + 15) // 16 * 16
+    h, g = rv.heads(x), rv.heads(d)
+    for f in (lambda: rv.kv8_append(c.c, h, g, 1, 1, None), lambda: rv.kv8_append(c.c, g, h, 1, 1, None),
+              lambda: rv.kv8_append(bad, g, g, 1, 1, None), lambda: rv.kv8_read(c.c, h, None, 1, 1, None),
+              lambda: rv.kv8_attention(c.c, h, g, 1, 1, 1.0, None, None, None, w.data_ptr(), need),
+              lambda: rv.kv8_attention(c.c, g, g, 1, 1, 1.0, None, None, None, w.data_ptr(), need - 1),
+              lambda: rv.kv8_attention(c.c, g, g, 1, 1, 1.0, None, None, None, None, need),
+              lambda: rv.kv8_attention(c.c, g, g, 1, 1, 1.0, None, None, None, bad.k_scale, need)):
+        with pytest.raises(rv.RVError) as e:
+            f()
+        assert e.value.code == rv.RV_EINVAL
+    for T in range(1, 17):  # the workspace of a larger call serves every smaller one
+        assert rv.kv8_attention_workspace(c.c, 1, T, 16) <= rv.kv8_attention_workspace(c.c, 1, 16, 16)
 
 
 def test_attention_strides_fp32_and_no_lse():

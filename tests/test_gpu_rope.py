@@ -153,3 +153,35 @@ def test_rope_captures_into_a_graph():
         torch.cuda.synchronize()
         at = np.array([start, 9])[:, None] + np.arange(T)
         check(y, x, rope(f64(x), at, freq, hd, False), 1.0, torch.float16)
+
+
+@pytest.mark.parametrize("B,T,H,hd,rot", [(1, 200003, 1, 16, 16), (70001, 3, 1, 64, 64), (2, 40000, 2, 128, 128)])
+def test_rope_many_tokens_of_few_heads(B, T, H, hd, rot):
+    """Runs of tokens that end inside a row and blocks that hold many rows."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(B, T, H, hd, generator=g, device="cuda")
+    pos = torch.randint(0, 1000, (B,), generator=g, device="cuda").to(torch.int32)
+    y = torch.empty_like(x)
+    rv.rope(plan_of(hd, rot, False), rv.heads(x), rv.heads(y), None, None, B, T, pos.data_ptr())
+    freq, _ = rope_frequencies(rot, 500000.0)
+    rows = sorted({0, B - 1, B // 2, min(B - 1, 1)})
+    at = pos.cpu().numpy()[rows][:, None] + np.arange(T)
+    check(y[rows], x[rows], rope(f64(x[rows]), at, freq, rot, False), 1.0, torch.float32)
+
+
+def test_rope_one_token_of_many_heads():
+    x = torch.randn(1, 2, 4096, 128).to(torch.bfloat16).cuda()
+    y = torch.empty_like(x)
+    rv.rope(plan_of(128, 64, True), rv.heads(x), rv.heads(y), None, None, 1, 2, None)
+    freq, _ = rope_frequencies(64, 500000.0)
+    check(y, x, rope(f64(x), [[0, 1]], freq, 64, True), 1.0, torch.bfloat16)
+
+
+def test_memory_that_is_not_the_devices_is_refused():
+    plan, x = plan_of(64, 64, False), torch.zeros(1, 1, 2, 64).cuda()
+    host = torch.zeros(1, 1, 2, 64)
+    pos = torch.zeros(1, dtype=torch.int32)
+    for a in ((host, x, None), (x, host, None), (x, x, pos.data_ptr())):
+        with pytest.raises(rv.RVError) as e:
+            rv.rope(plan, rv.heads(a[0]), rv.heads(a[1]), None, None, 1, 1, a[2])
+        assert e.value.code == rv.RV_EINVAL

@@ -139,6 +139,8 @@ def test_rope_refusals():
     refused(rv.rope, p, f, h, None, None, 1, 1, None)                   # in place with two types
     refused(rv.rope, p, h, h, f, f, 1, 1, None)
     refused(rv.rope, p, h, h, None, None, 1, 1, OK + 2)
+    big = heads(n=4096)
+    refused(rv.rope, p, big, big, h, h, 1, 1, None)                     # 4104 heads of 128
     refused(rv.rope, p, h, h, None, None, 1, 1, None, OK + 1)
 
 

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(512) k_append(Kv8 c, Kv8Io io, int log_block) 
   const int end = (int)min((int64_t)pos + n, (int64_t)c.T);
   if (pos < 0 || end - pos < n) {  // not a position of the cache, or some tokens are not
     if (io.err && blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) atomicOr(io.err, kKv8ErrPos);
-    if (pos < 0) return;
+    if (pos < 0 || pos >= c.T) return;
   }
   const int blk = (pos >> log_block) + blockIdx.x, p0 = blk << log_block;
   if (p0 >= end) return;

@@ -71,7 +71,7 @@ __host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes
 // 2^kLag are as good in fp16 and fp32, and a tile that raises no maximum needs
 // no reduction over the warp and no rescaling.  kUnseen: nothing seen yet
 // (finite, so that -m stays an ordinary addend).
-constexpr float kLag = 8.f, kUnseen = -1e30f;
+constexpr float kLag = 8.f, kUnseen = -3.402823466e38f;
 // One cut unit's state: O [rows][hd], then m and l [rows].
 __host__ __device__ constexpr size_t slot_floats(int hd, int nt) { return (size_t)8 * nt * (hd + 2); }
 
@@ -899,7 +899,13 @@ __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8A
   pdl_trigger();
   const Cut *cuts = static_cast<const Cut *>(a.work);
   const float *work = reinterpret_cast<const float *>(cuts + pieces);
-  const Cut cut = cuts[blockIdx.x];
+  union {
+    int4 v[2];
+    Cut cut;
+  } u;
+  u.v[0] = __ldcg(reinterpret_cast<const int4 *>(cuts + blockIdx.x));
+  u.v[1] = __ldcg(reinterpret_cast<const int4 *>(cuts + blockIdx.x) + 1);
+  const Cut cut = u.cut;
   const int b = cut.b, c0 = cut.c0, c1 = cut.last;
   if (c1 == 0) return;
   const int rr = blockIdx.y * RPB + warp / WPR, row = cut.row0 + rr, sub = warp % WPR;

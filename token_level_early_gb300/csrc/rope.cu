@@ -256,6 +256,7 @@ cudaError_t launch_io(const rv_rope_plan &plan, const RopeArgs &a, cudaStream_t 
   // as many tokens as the threads' first items cover, but enough blocks to fill the GPU
   int tpb = kThreads * (IN == RV_F32 ? 2 : 4) / items;
   if (tpb > tokens / 608) tpb = tokens / 608;
+  if (tpb > 4096 / pairs) tpb = 4096 / pairs;  // 32 KB of sines and cosines
   if (tpb < 1) tpb = 1;
   g.tokens_per_block = tpb;
   g.items = fast_div(items);
@@ -369,6 +370,9 @@ extern "C" int rv_rope(const rv_rope_plan *plan, const rv_heads *q_in, const rv_
   if (k_in && (check_heads("k_in", k_in, B, T, hd, false) || check_heads("k_out", k_out, B, T, hd, true))) return RV_EINVAL;
   if (q_in->heads != q_out->heads || (k_in && k_in->heads != k_out->heads)) return op_fail(RV_EINVAL, "in and out differ in heads");
   if (k_in && (k_in->dtype != q_in->dtype || k_out->dtype != q_out->dtype)) return op_fail(RV_EINVAL, "q and k differ in dtype");
+  // the kernel's quotients of a token's 16-element chunks are exact up to here
+  if ((int64_t)(q_in->heads + (k_in ? k_in->heads : 0)) * (hd / 16) > 32768)
+    return op_fail(RV_EINVAL, "query and key heads x head_dim above 2^19 elements a token");
   if (q_in->dtype != q_out->dtype && q_in->dtype != RV_F32) return op_fail(RV_EINVAL, "a 16-bit input keeps its dtype");
   if (q_in->data == q_out->data && q_in->dtype != q_out->dtype) return op_fail(RV_EINVAL, "in place needs one dtype");
   if (k_in && k_in->data == k_out->data && k_in->dtype != k_out->dtype) return op_fail(RV_EINVAL, "in place needs one dtype");
