@@ -444,8 +444,9 @@ int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_ou
  * nothing is seen), with which partial results over several caches can be
  * merged.  Scores, softmax and sums are fp32; the probabilities enter the
  * product with V as fp16.  workspace: rv_kv8_attention_workspace bytes,
- * 16-byte aligned, no contents needed or kept; calls that may run at the
- * same time (other streams, graphs replayed concurrently) need one each. */
+ * 16-byte aligned, no contents needed or kept (short contexts may not use
+ * it); calls that may run at the same time (other streams, graphs replayed
+ * concurrently) need one each. */
 int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, float scale,
                      const int32_t *d_pos, const int32_t *d_count, float *d_lse, void *workspace,
                      size_t workspace_bytes, void *stream);

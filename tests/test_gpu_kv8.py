@@ -291,8 +291,15 @@ def check_attention(c, kk, vv, q, scale, pos, count, out, lse):
                 assert abs(gl - rl) <= lse_tolerance(rl, D), (b, t, h, gl, rl)
 
 
-def filled(B, Hkv, hd, block, fmt, act, lens, max_seq, seed=1):
-    c = Cache(B, Hkv, hd, max_seq, block, fmt, act)
+@pytest.fixture(params=[0, 70000], ids=["cluster", "line"])
+def room(request):
+    """Smallest max_seq of a test's caches: small caches run the attention's
+    cluster plan, large ones (however little they hold) the cut line."""
+    return request.param
+
+
+def filled(B, Hkv, hd, block, fmt, act, lens, max_seq, seed=1, room=0):
+    c = Cache(B, Hkv, hd, max(max_seq, room), block, fmt, act)
     T = max(max(lens), 1)
     k, v = data(seed, B, T, Hkv, hd, act, False), data(seed + 1, B, T, Hkv, hd, act, False)
     k[..., 3] *= 6.0
@@ -306,10 +313,10 @@ def filled(B, Hkv, hd, block, fmt, act, lens, max_seq, seed=1):
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("hd", [64, 128])
 @pytest.mark.parametrize("block", [16, 32, 64, 128])
-def test_attention_types_and_blocks(block, hd, fmt, act):
+def test_attention_types_and_blocks(block, hd, fmt, act, room):
     lens = [1, 31, 200, 130]
     B, Hkv, H = 4, 2, 8
-    c, kk, vv = filled(B, Hkv, hd, block, fmt, act, lens, 205)
+    c, kk, vv = filled(B, Hkv, hd, block, fmt, act, lens, 205, room=room)
     q = data(9, B, 1, H, hd, act, False)
     pos = [n - 1 for n in lens]
     out, lse = c.attention(q, hd ** -0.5, pos)
@@ -318,12 +325,12 @@ def test_attention_types_and_blocks(block, hd, fmt, act):
 
 @pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 3), (8, 1), (7, 1), (16, 1), (20, 1), (10, 2), (32, 8)])
 @pytest.mark.parametrize("T", [1, 2, 5, 16])
-def test_attention_head_layouts_and_drafted_tokens(T, H, Hkv):
+def test_attention_head_layouts_and_drafted_tokens(T, H, Hkv, room):
     """Query rows of every count per KV head (T x H / Hkv from 1 to 320), with
     ragged counts and rows that see little or nothing."""
     lens, act, hd = [300, 17, T, 97], 1, 64
     B = 4
-    c, kk, vv = filled(B, Hkv, hd, 32, 0, act, lens, 320)
+    c, kk, vv = filled(B, Hkv, hd, 32, 0, act, lens, 320, room=room)
     q = data(10, B, T, H, hd, act, False)
     pos = [300 - T, 17 - T, -2, 97 - T]
     count = [T, max(T - 1, 1), T, 0]
@@ -332,31 +339,31 @@ def test_attention_head_layouts_and_drafted_tokens(T, H, Hkv):
 
 
 @pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 511, 1000, 2047, 2049, 5000])
-def test_attention_lengths(n):
-    c, kk, vv = filled(1, 1, 128, 64, 0, 1, [n], n)
+def test_attention_lengths(n, room):
+    c, kk, vv = filled(1, 1, 128, 64, 0, 1, [n], n, room=room)
     q = data(11, 1, 1, 4, 128, 1, False)
     out, lse = c.attention(q, 128 ** -0.5, [n - 1])
     check_attention(c, kk, vv, q, 128 ** -0.5, [n - 1], None, out, lse)
 
 
-def test_attention_many_rows_of_unequal_length():
+def test_attention_many_rows_of_unequal_length(room):
     B, Hkv, H, hd = 37, 3, 6, 64
     g = np.random.default_rng(2)
     lens = [int(x) for x in g.integers(1, 400, B)]
     lens[5], lens[20] = 1, 1900
-    c, kk, vv = filled(B, Hkv, hd, 16, 1, 0, lens, 1900)
+    c, kk, vv = filled(B, Hkv, hd, 16, 1, 0, lens, 1900, room=room)
     q = data(12, B, 1, H, hd, 0, False)
     pos = [n - 1 for n in lens]
     out, lse = c.attention(q, 0.125, pos)
     check_attention(c, kk, vv, q, 0.125, pos, None, out, lse)
 
 
-def test_attention_ignores_what_lies_behind():
+def test_attention_ignores_what_lies_behind(room):
     """Codes and scales behind a row's last visible position are junk (NaN
     codes, NaN scales in this cache's first filling); a block poisoned by a
     NaN reaches the rows that see it and no others."""
     Hkv, hd, block = 2, 64, 32
-    c, kk, vv = filled(2, Hkv, hd, block, 1, 1, [40, 70], 96)
+    c, kk, vv = filled(2, Hkv, hd, block, 1, 1, [40, 70], 96, room=room)
     q = data(13, 2, 2, 4, hd, 1, False)
     out, lse = c.attention(q, 0.125, [38, 68])
     check_attention(c, kk, vv, q, 0.125, [38, 68], None, out, lse)
@@ -364,7 +371,7 @@ def test_attention_ignores_what_lies_behind():
     v = data(17, 1, 64, Hkv, hd, 1, False)
     k = data(18, 1, 64, Hkv, hd, 1, False)
     k[0, 33, 1, 0] = math.inf
-    c2 = Cache(1, Hkv, hd, 64, block, 0, 1)
+    c2 = Cache(1, Hkv, hd, max(64, room), block, 0, 1)
     c2.append(k, v, [0])
     q = data(19, 1, 4, 4, hd, 1, False)
     out, lse = c2.attention(q, 0.125, [30])                                # tokens see 31, 32, 33, 34 positions
@@ -378,7 +385,7 @@ def test_attention_ignores_what_lies_behind():
             assert (np.abs(f64(out)[0, t, h] - ref) <= bound("bfloat16")).all() and abs(float(lse[0, t, h]) - rl) <= lse_tolerance(rl, D)
 
 
-def test_attention_blocks_of_very_different_scales():
+def test_attention_blocks_of_very_different_scales(room):
     """Scales of neighbouring blocks that differ by 2^60: the weights decide,
     not the sizes of the scales."""
     hd, block = 64, 16
@@ -390,23 +397,23 @@ def test_attention_blocks_of_very_different_scales():
     k[0, 32:48, 0, 0] = -1e4   # so that what is large has no weight
     q = data(22, 1, 1, 2, hd, 1, False)
     q[..., 0] = 4.0
-    c = Cache(1, 1, hd, 64, block, 0, 1)
+    c = Cache(1, 1, hd, max(64, room), block, 0, 1)
     c.append(k, v, [0])
     kk, vv = [expect(c, f64(k)[0], 64)[0]], [expect(c, f64(v)[0], 64)[0]]
     out, lse = c.attention(q, 0.5, [63])
     check_attention(c, kk, vv, q, 0.5, [63], None, out, lse)
 
 
-def test_attention_large_and_small_queries():
+def test_attention_large_and_small_queries(room):
     """Queries near the ends of bf16's range, scale 0 and a negative scale."""
-    c, kk, vv = filled(1, 1, 64, 16, 0, 1, [50], 64)
+    c, kk, vv = filled(1, 1, 64, 16, 0, 1, [50], 64, room=room)
     for mul, scale in ((2.0 ** 100, 2.0 ** -103), (2.0 ** -100, 2.0 ** 97), (1.0, 0.0), (1.0, -0.125)):
         q = data(23, 1, 2, 3, 64, 1, False) * mul
         out, lse = c.attention(q, scale, [48])
         check_attention(c, kk, vv, q, scale, [48], None, out, lse)
 
 
-def test_attention_scores_far_from_zero():
+def test_attention_scores_far_from_zero(room):
     """Scores around +-1e4 and rows whose maxima rise from tile to tile: the
     reference of the weights has to follow."""
     hd, n, block = 64, 700, 32
@@ -417,7 +424,7 @@ def test_attention_scores_far_from_zero():
         v = data(31, 1, n, 1, hd, 1, False)
         q = data(32, 1, 2, 2, hd, 1, False)
         q[..., 0] = 50.0
-        c = Cache(1, 1, hd, n, block, 1, 1)
+        c = Cache(1, 1, hd, max(n, room), block, 1, 1)
         k = k.to(torch.bfloat16).cuda()
         c.append(k, v, [0])
         kk, vv = [expect(c, f64(k)[0], n)[0]], [expect(c, f64(v)[0], n)[0]]
@@ -448,9 +455,9 @@ def test_calls_refuse_what_is_not_device_memory():
         assert rv.kv8_attention_workspace(c.c, 1, T, 16) <= rv.kv8_attention_workspace(c.c, 1, 16, 16)
 
 
-def test_attention_strides_fp32_and_no_lse():
+def test_attention_strides_fp32_and_no_lse(room):
     B, T, H, hd = 2, 3, 4, 64
-    c, kk, vv = filled(B, 2, hd, 16, 0, 1, [90, 33], 96)
+    c, kk, vv = filled(B, 2, hd, 16, 0, 1, [90, 33], 96, room=room)
     wide = torch.randn(B, H, T, hd + 8, generator=torch.Generator().manual_seed(1)).cuda()
     q = wide[..., :hd].transpose(1, 2)          # fp32, rounded to bf16 by the call
     qr = q.to(torch.bfloat16)
@@ -465,8 +472,8 @@ def test_attention_strides_fp32_and_no_lse():
     assert (lse == 7.0).all() and torch.equal(o2, o.contiguous())
 
 
-def test_attention_repeats_bit_for_bit():
-    c, _, _ = filled(3, 2, 128, 64, 0, 1, [3000, 700, 64], 3000)
+def test_attention_repeats_bit_for_bit(room):
+    c, _, _ = filled(3, 2, 128, 64, 0, 1, [3000, 700, 64], 3000, room=room)
     q = data(24, 3, 2, 8, 128, 1, False)
     a = c.attention(q, 0.1, [2998, 698, 62])
     for _ in range(3):
@@ -474,7 +481,7 @@ def test_attention_repeats_bit_for_bit():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_decode_run_with_all_operators_and_graphs():
+def test_decode_run_with_all_operators_and_graphs(room):
     """A generation as a program runs it: rotate, append, attend, one token at
     a time, the three calls captured once into a graph per stream and replayed
     with positions that move on the device; two such programs run at the same
@@ -483,7 +490,7 @@ def test_decode_run_with_all_operators_and_graphs():
     plan = rv.rope_plan(hd, hd, rv.ROPE_HALF, 10000.0)
     progs = []
     for i in range(2):
-        p = {"c": Cache(1, Hkv, hd, T0 + steps, block, i, act), "pos": torch.zeros(1, dtype=torch.int32).cuda(), "s": torch.cuda.Stream()}
+        p = {"c": Cache(1, Hkv, hd, max(T0 + steps, room), block, i, act), "pos": torch.zeros(1, dtype=torch.int32).cuda(), "s": torch.cuda.Stream()}
         kv = data(30 + i, 1, T0 + steps, Hkv, hd, act, False), data(40 + i, 1, T0 + steps, Hkv, hd, act, False)
         q = data(50 + i, 1, T0 + steps, H, hd, act, False)
         p.update(kv=kv, q=q, in_q=q[:, :1].clone(), in_k=kv[0][:, :1].clone(), in_v=kv[1][:, :1].clone())
@@ -527,3 +534,26 @@ def test_decode_run_with_all_operators_and_graphs():
             vv = [expect(p["c"], f64(p["kv"][1])[0], n)[0]]
             rq, out, lse = got[j][i]
             check_attention(p["c"], kk, vv, rq, hd ** -0.5, [n - 1], None, out, lse)
+
+
+def test_rows_behind_32_bit_offsets():
+    """A cache of 5.4 GB of K codes: its last row lies behind every 32-bit
+    offset; the rows before it see one position each or nothing."""
+    B, Hkv, hd, block, n = 40, 8, 128, 64, 150
+    c = Cache(B, Hkv, hd, 131072, block, 0, 1)
+    assert c.codes[0].numel() > 2 ** 32
+    k, v = data(41, 1, n, Hkv, hd, 1, False), data(42, 1, n, Hkv, hd, 1, False)
+    kb, vb = (x.expand(B, n, Hkv, hd) for x in (k, v))          # every row the same tokens, stride 0
+    count = [1] * (B - 2) + [0, n]
+    c.append(kb, vb, [0] * B, count)
+    got = c.read([0] * B, n, count=count)
+    for x, src in zip(got, (k, v)):
+        assert np.array_equal(f64(x)[B - 1], expect(c, f64(src)[0], n)[0])
+        assert np.array_equal(f64(x)[0, :1], expect(c, f64(src)[0], 1)[0])
+    del got
+    q = data(43, B, 1, 2 * Hkv, hd, 1, False)
+    pos = [0] * (B - 2) + [-1, n - 1]
+    kk = [expect(c, f64(k)[0], max(m, 1))[0] for m in count]
+    vv = [expect(c, f64(v)[0], max(m, 1))[0] for m in count]
+    out, lse = c.attention(q, 0.1, pos)
+    check_attention(c, kk, vv, q, 0.1, pos, None, out, lse)

@@ -299,6 +299,14 @@ cudaError_t kv8_append_staged(const rv_model *m, int l, const KVGeom &g, int B, 
   return launch_kv8_append(kv8_layer(m, l), io, m->act, s, 1);
 }
 
+// The attention's plan for rows 0..B-1 at their current positions (captured
+// steps are keyed by it).
+int kv8_plan(const rv_model *m, int B) {
+  int most = 0;
+  for (int b = 0; b < B && b < (int)m->h_len.size(); ++b) most = std::max(most, m->h_len[b] + 1);
+  return kv8_attention_cluster(m->kv8, B, 1, m->H, m->n_sm, std::min(most, m->Tmax));
+}
+
 // One token per row: q and o are fp32 rows of act16-rounded values.
 cudaError_t kv8_attend(const rv_model *m, int l, const float *q, float *o, int B, const int32_t *pos, cudaStream_t s, int pdl) {
   Kv8AttnArgs a{};
@@ -313,6 +321,7 @@ cudaError_t kv8_attend(const rv_model *m, int l, const float *q, float *o, int B
   a.scale = 1.0f / sqrtf((float)m->hd);
   a.pos = pos;
   a.work = m->kv8_work;
+  a.cluster = kv8_plan(m, B);
   return launch_kv8_attention(a, m->n_sm, s, pdl);
 }
 
@@ -661,7 +670,7 @@ int launch_step(rv_model *m, int B) {
     RV_CK(stream_launch(m->sargs, m->stream_grid, m->stream));
     return RV_OK;
   }
-  const int key = 2 * B + (m->kv_mode ? 0 : attn_plan(m, B, nullptr));
+  const int key = m->kv_mode ? 16 * B + kv8_plan(m, B) : 2 * B + attn_plan(m, B, nullptr);
   auto it = m->graphs.find(key);
   if (it == m->graphs.end()) {
     if (B > 1) {

@@ -471,5 +471,6 @@ extern "C" int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv
   a.pos = d_pos; a.count = d_count;
   a.lse = d_lse;
   a.work = workspace;
+  a.cluster = kv8_attention_cluster(c, B, T, a.H, n_sm, c.T);
   return launched("rv_kv8_attention", launch_kv8_attention(a, n_sm, static_cast<cudaStream_t>(stream), 1));
 }

@@ -21,6 +21,26 @@ cudaError_t launch_int8(const Kv8AttnArgs &a, int nt, int n_sm, cudaStream_t s, 
 
 }  // namespace kv8a
 
+// The cluster plan for short contexts: enough blocks for two tiles each while
+// the units' clusters fit one block per SM, more (two per SM) where a block
+// would have over 16 tiles; the line where it still has.  Measured in
+// microseconds, line / clusters of 1 / 2 / 4 / 8 (bf16, head_dim 128, one row
+// of 8 KV heads): 256 positions 9.7 / 6.9 / 5.8 / 5.2 / 5.4, 1024: 10.1 / 11.2
+// / 8.1 / 6.7 / 6.0, 4096: 11.3 / 28 / 17 / 11.0 / 8.1, 8192: 12.9 / - / - /
+// 16.5 / 11.0; 16 such rows: 256: 17.9 / 6.8 / 6.3 / 11.3 / 22, 1024: 11.9 /
+// 11.1 / 9.3 / 13.8 / 23, 2048: 13.6 / 16.8 / 13.5 / 16 / 25, 4096: 20.4 / 30 /
+// 21 / 24 / 33; one KV head: 2048: 7.7 / 17 / 11 / 8.2 / 6.7, 4096: 7.7 / 29 /
+// 17 / 11 / 8.1.
+int kv8_attention_cluster(const Kv8 &c, int B, int T, int H, int n_sm, int most) {
+  const int rows = T * (H / c.Hkv), nt = kv8a::pick_nt(rows);
+  const int64_t tiles = (most + kv8a::tile_len(c.hd) - 1) / kv8a::tile_len(c.hd);
+  const int64_t units = (int64_t)B * c.Hkv * ((rows + 8 * nt - 1) / (8 * nt));
+  int cs = 1;
+  while (cs < 8 && tiles > 2 * cs && units * cs * 2 <= n_sm) cs *= 2;
+  while (cs < 8 && tiles > 16 * cs && units * cs * 2 <= 2 * n_sm) cs *= 2;
+  return tiles <= 16 * cs && units <= INT32_MAX / 8 ? cs : 0;
+}
+
 size_t kv8_attention_work(const Kv8 &c, int, int T, int H, int n_sm) {
   // a smaller T may run fewer columns (and then more blocks): the largest need
   const int cols = (T * (H / c.Hkv) + 7) / 8;

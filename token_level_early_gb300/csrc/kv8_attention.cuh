@@ -27,7 +27,9 @@
 // lengths: a block computes its own piece of the line from d_pos, finishes
 // the units that lie in it and leaves the state (m, l, O) of at most two cut
 // ones, which a second kernel, chained by programmatic dependent launch,
-// joins.  fp16 caches split each weight into a high and a low fp16 term.
+// joins.  Short contexts take a cluster per unit instead, which joins through
+// distributed shared memory.  fp16 caches split each weight into a high and a
+// low fp16 term.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -42,7 +44,8 @@ constexpr int kWarps = 4;  // warps of a block
 __host__ __device__ constexpr int tile_len(int hd) { return hd == 128 ? 32 : 64; }
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// Smallest piece of the line a block takes: one tile for each of its warps.
+// Smallest piece of the line a block takes: one tile for each of its warps
+// (a unit where units are shorter: short ones side by side, not in a row).
 constexpr int kMinTiles = kWarps;
 // What beginning a unit costs a block, in tiles (its queries' operands, the
 // join of the warps): the line counts it, where pieces are long enough.
@@ -215,6 +218,39 @@ __device__ __forceinline__ int v_off(int p, int c) {
 
 // ------------------------------------------------------------------ main kernel
 
+__device__ __forceinline__ unsigned cluster_blocks() {
+  unsigned n;
+  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ unsigned cluster_rank() {
+  unsigned n;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of the cluster's block k at the address that `at` is here.
+__device__ __forceinline__ unsigned map_cluster(unsigned at, int k) {
+  unsigned r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(at), "r"(k));
+  return r;
+}
+__device__ __forceinline__ float ld_cluster(unsigned at, int k) {
+  float x;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_cluster(at, k)) : "memory");
+  return x;
+}
+__device__ __forceinline__ float4 ld_cluster4(unsigned at, int k) {
+  float4 x;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+               : "r"(map_cluster(at, k))
+               : "memory");
+  return x;
+}
+
 // 4 elements of an output row from its joined state (x = weighted sum, mm =
 // maximum in base 2, ll = sum).
 __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, int h, int d, float4 x, float mm, float ll) {
@@ -244,7 +280,10 @@ struct Segment {
 
 // GS: 16-position steps of a tile that share a scale (the smaller of block and
 // tile).  LO: the weights enter as two fp16 terms (high and low part).
-template <int FMT, int HD, int NT, int GS, bool LO>
+// CL: short contexts; a cluster takes one unit, its blocks cut the unit's
+// tiles evenly and join through distributed shared memory: no workspace and
+// no second kernel.
+template <int FMT, int HD, int NT, int GS, bool LO, bool CL>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(const __grid_constant__ Kv8AttnArgs a, int by_unit) {
   constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = stages(NT), SB = stage_bytes(HD);
   constexpr int TL = tile_len(HD), TM = TL / 16, NG = TM / GS;
@@ -261,11 +300,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   const int grp = a.H / c.Hkv, groups = (a.T * grp + ROWS - 1) / ROWS;
   Cut *cuts = static_cast<Cut *>(a.work);
   float *slots = reinterpret_cast<float *>(cuts + gridDim.x) + (size_t)2 * blockIdx.x * slot_floats(HD, NT);
-  if (tid == 0 && !by_unit) cuts[blockIdx.x].last = 0;
+  if (!CL && tid == 0 && !by_unit) cuts[blockIdx.x].last = 0;
   // rows that see nothing have no tiles: zeros
   for (int i = blockIdx.x; i < a.B; i += gridDim.x) {
     const Row r = row_of<HD>(a, i, ROWS);
-    if (by_unit)
+    if (!CL && by_unit)
       for (int u = tid; u < c.Hkv * groups; u += kWarps * 32)
         if (!r.tiles || u % groups >= r.groups) cuts[(int64_t)i * c.Hkv * groups + u].last = 0;
     if (r.n) continue;
@@ -277,9 +316,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 
   // ---- this block's piece [begin, end) of the line, and where it begins:
   // `off` into row `b`.  A unit takes `extra` + its tiles of the line.
-  int64_t total, piece, begin, end, off = 0;
-  int b = 0, extra;
-  {
+  int64_t total = 0, piece = 1, begin = 0, end = 0, off = 0;
+  int b = 0, extra = 0;
+  const int ranks = CL ? (int)cluster_blocks() : 1, rank = CL ? (int)cluster_rank() : 0;
+  if (!CL) {
     // each thread sums a run of rows; the one whose run holds `begin` finds the row
     const int per = (a.B + kWarps * 32 - 1) / (kWarps * 32), r0 = min(a.B, tid * per), r1 = min(a.B, r0 + per);
     int64_t tiles = 0, units = 0, all_tiles = 0, all_units = 0, tiles_before = 0, units_before = 0;
@@ -312,7 +352,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     extra = all_tiles >= (int64_t)gridDim.x * 2 * kWarps ? kUnitTiles : 0;
     total = all_tiles + extra * all_units;
     piece = (total + gridDim.x - 1) / gridDim.x;
-    if (piece < kMinTiles) piece = kMinTiles;
+    if (piece < kMinTiles && all_units) piece = max(piece, min((int64_t)kMinTiles, (all_tiles + all_units - 1) / all_units));
     begin = piece * blockIdx.x;
     if (begin >= total) return;
     end = min(total, begin + piece);
@@ -339,8 +379,23 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 
   // ---- segments, one ahead of the one that is worked on
   int64_t left = end - begin;
+  if (CL) b = blockIdx.x / ranks / (c.Hkv * groups);
   Row r = row_of<HD>(a, b, ROWS);
   auto next_segment = [&](Segment &s) {
+    if (CL) {  // one segment: this block's share of the cluster's unit (it may be empty)
+      const int unit = blockIdx.x / ranks - b * c.Hkv * groups, per = (r.tiles + ranks - 1) / ranks;
+      s.b = b;
+      s.g = unit / groups;
+      s.row0 = (unit - s.g * groups) * ROWS;
+      s.t0 = min(r.tiles, rank * per);
+      s.t1 = min(r.tiles, s.t0 + per);
+      s.n = r.n;
+      s.count = r.count;
+      s.tiles = r.tiles;
+      s.rows = (int64_t)b * c.Hkv + s.g;
+      left = 0;
+      return r.tiles > 0 && unit - s.g * groups < r.groups;
+    }
     for (;;) {
       if (left <= 0) return false;
       const int64_t in_row = (int64_t)row_units(a, r) * (r.tiles + extra);
@@ -385,8 +440,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   // groups always covers the tile at hand.
   Segment cur, nxt;
   if (!next_segment(cur)) return;
-  bool more = next_segment(nxt);
-  auto tiles_of = [&](const Segment &s) { return (s.t1 - s.t0 - warp + kWarps - 1) / kWarps; };  // >= 0: t1 > t0, and -3 / 4 = 0
+  bool more = !CL && next_segment(nxt);
+  auto tiles_of = [&](const Segment &s) { return (s.t1 - s.t0 - warp + kWarps - 1) / kWarps; };  // >= 0: -3 / 4 = 0
   int cnt = tiles_of(cur), ncnt = more ? tiles_of(nxt) : 0;
   int filled[2] = {0, 0}, fill[2] = {0, 0}, head = 0;  // [K, V]: tiles asked for from the current segment on, and the slot of the next
   // Asks for the next tile's K (which = 0) or V rows and scales.
@@ -803,6 +858,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     }
 
     // ---- join the warps' states
+    if (CL) cp_wait<0>();
     __syncthreads();  // the states of the segment before have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -819,9 +875,9 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         }
       }
     }
-    const bool whole = cur.t0 == 0 && cur.t1 == cur.tiles;
+    const bool whole = !CL && cur.t0 == 0 && cur.t1 == cur.tiles;
     float *slotp = slots + (first ? 0 : slot_floats(HD, NT));
-    if (tid == 0 && cur.t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
+    if (!CL && tid == 0 && cur.t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
       const int64_t at = by_unit ? cur.rows * groups + cur.row0 / ROWS : blockIdx.x;
       cuts[at] = Cut{cur.b, cur.g, cur.row0, (int)blockIdx.x, whole ? 0 : (int)(cur.last / piece), first ? 0 : 1, {0, 0}};
     }
@@ -857,6 +913,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           ll = fmaf(s_l[w][rr], f, ll);
           x.x = fmaf(y.x, f, x.x); x.y = fmaf(y.y, f, x.y); x.z = fmaf(y.z, f, x.z); x.w = fmaf(y.w, f, x.w);
         }
+        if (CL) slotp = reinterpret_cast<float *>(sm);  // the rings are idle
         if (!whole) {
           *reinterpret_cast<float4 *>(slotp + rr * HD + d) = x;
           if (d == 0) {
@@ -868,6 +925,30 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
           write_out(a, cur.b, t, h, d, x, mm, ll);
         }
       }
+    }
+    if (CL) {
+      // every block of the cluster has left its state in shared memory: each
+      // joins a part of the elements
+      cluster_sync();
+      for (int u = rank * kWarps * 32 + tid; u < ROWS * (HD / 4); u += ranks * kWarps * 32) {
+        const int rr = u / (HD / 4), d = (u - rr * (HD / 4)) * 4, row = cur.row0 + rr;
+        if (row >= nrows) break;
+        const unsigned at = (unsigned)__cvta_generic_to_shared(sm);
+        float mm = -INFINITY, ll = 0.f;
+        float4 x = make_float4(0, 0, 0, 0);
+        for (int k = 0; k < ranks; ++k) mm = fmaxf(mm, ld_cluster(at + 4 * (ROWS * HD + rr), k));
+        const float base = mm == -INFINITY ? 0.f : mm;
+        for (int k = 0; k < ranks; ++k) {
+          const float f = ex2(ld_cluster(at + 4 * (ROWS * HD + rr), k) - base);
+          const float4 y = ld_cluster4(at + 4 * (rr * HD + d), k);
+          ll = fmaf(ld_cluster(at + 4 * (ROWS * HD + ROWS + rr), k), f, ll);
+          x.x = fmaf(y.x, f, x.x); x.y = fmaf(y.y, f, x.y); x.z = fmaf(y.z, f, x.z); x.w = fmaf(y.w, f, x.w);
+        }
+        const int t = row / grp, h = cur.g * grp + row - t * grp;
+        write_out(a, cur.b, t, h, d, x, mm, ll);
+      }
+      cluster_sync();  // no block leaves while another reads its state
+      break;
     }
     if (!more) break;
     // ---- on to the next segment, part of whose tiles are on their way
@@ -980,11 +1061,32 @@ __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8A
 
 template <int FMT, int HD, int NT, int GS, bool LO>
 cudaError_t launch_t(const Kv8AttnArgs &a, int n_sm, cudaStream_t s, int pdl) {
-  auto fn = k_attn8<FMT, HD, NT, GS, LO>;
+  const int rows = a.T * (a.H / a.c.Hkv);
+  const int64_t units = (int64_t)a.B * a.c.Hkv * ((rows + 8 * NT - 1) / (8 * NT));
+  if (a.cluster) {
+    auto fn = k_attn8<FMT, HD, NT, GS, LO, true>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(HD, NT));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * a.cluster));
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = smem_bytes(HD, NT);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, fn, a, 0);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  auto fn = k_attn8<FMT, HD, NT, GS, LO, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(HD, NT));
   if (e != cudaSuccess) return e;
-  const int pieces = blocks_per_sm(HD, NT) * n_sm, rows = a.T * (a.H / a.c.Hkv);
-  const int64_t units = (int64_t)a.B * a.c.Hkv * ((rows + 8 * NT - 1) / (8 * NT));
+  const int pieces = blocks_per_sm(HD, NT) * n_sm;
   const int by_unit = units <= pieces, cuts = by_unit ? (int)units : pieces;
   e = launch_k(fn, dim3(pieces), dim3(kWarps * 32), smem_bytes(HD, NT), s, pdl, a, by_unit);
   if (e != cudaSuccess) return e;

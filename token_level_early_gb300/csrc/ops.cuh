@@ -127,7 +127,10 @@ struct Kv8AttnArgs {
   const int32_t *pos, *count;
   float *lse;
   void *work;
+  int cluster;  // blocks of a cluster (short contexts: a cluster per unit), or 0 (the cut line)
 };
+// Kv8AttnArgs::cluster for rows that see up to `most` positions.
+int kv8_attention_cluster(const Kv8 &c, int B, int T, int H, int n_sm, int most);
 size_t kv8_attention_work(const Kv8 &c, int B, int T, int H, int n_sm);
 cudaError_t launch_kv8_attention(const Kv8AttnArgs &a, int n_sm, cudaStream_t s, int pdl = 0);
 
