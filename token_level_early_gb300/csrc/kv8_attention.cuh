@@ -20,8 +20,8 @@
 // consecutive bytes of four V rows as its part of two positions' pairs.
 //
 // Memory bounds it: 2 head_dim bytes per position and KV head, read once.
-// Each warp streams its own tiles of 32 positions (8 KB at head_dim 128)
-// through a private ring in shared memory (cp.async, no barriers inside a
+// Each warp streams its own tiles of 8 KB (32 positions at head_dim 128, 64 at
+// 64) through a private ring in shared memory (cp.async, no barriers inside a
 // segment).  The (row, KV head, row group) units with their tiles form one
 // line that is cut evenly over the resident blocks, whatever the rows'
 // lengths: a block computes its own piece of the line from d_pos, finishes
@@ -30,6 +30,13 @@
 // joins.  Short contexts take a cluster per unit instead, which joins through
 // distributed shared memory.  fp16 caches split each weight into a high and a
 // low fp16 term.
+//
+// Measured on a GB300 (graph of passes, inputs larger than L2): one row of
+// 131,000 positions, 8 KV heads of 128: 47 us = 5.7 TB/s, 85% of a copy's rate
+// (a kernel that only reads the same bytes through the same rings takes 41
+// us; the joining kernel is 3 to 4 of the difference); 64 ragged rows of the
+// 1B shape: 55 us = 5.6 TB/s.  With 24 query rows per KV head instruction
+// issue bounds it (about 1250 a tile, 34% of cycles): 54 us for 149 MB.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -51,24 +58,26 @@ constexpr int kMinTiles = kWarps;
 // join of the warps): the line counts it, where pieces are long enough.
 constexpr int kUnitTiles = 8;
 
-// Blocks per SM, as many as the registers leave room for; the tiles of a
-// warp's ring (K and V have their own slots: one tile still keeps a half on
-// its way while the other is worked on); query operands in shared memory or
-// in registers.  Measured for up to 8 rows, blocks / ring / operands: head_dim
-// 64, ragged batch of 64: 3/1/shared 56.8 us, 3/2/registers 59.9, 4/1/shared
-// 59.3; head_dim 128, 131K positions: 2/1/registers 50.1 us, 2/2/registers
-// 51.7, 3/1/shared 51.8, 4/1/shared 61.6 (spills).
+// Blocks per SM, as many as the registers leave room for; tiles of a warp's
+// ring (K and V have their own slots: with one tile a half of it is on its way
+// while the other is worked on); query operands in shared memory or in
+// registers.  Measured, blocks / ring / operands: up to 8 rows, head_dim 64,
+// ragged batch of 64: 3/1/shared 56.8 us, 3/2/registers 59.9, 4/1/shared 59.3;
+// head_dim 128, 131K positions: 2/1/registers 50.1 us, 2/2/registers 51.7,
+// 3/1/shared 51.8, 4/1/shared 61.6 (spills); 16 rows of 9000 positions: 2/1
+// 41.9 us, 2/2 45.0; 24 rows: 2/1 45.8, 2/2 47.8.  Blocks of 8 warps, half as
+// many: 54.6 and 58.0 us there; of 2 warps, twice as many: 42.8 and 49.2.
 __host__ __device__ constexpr int blocks_per_sm(int hd, int nt) { return nt == 1 && hd == 64 ? 3 : 2; }
-__host__ __device__ constexpr int stages(int nt) { return nt == 1 ? 1 : 2; }
+constexpr int kStages = 1;
 __host__ __device__ constexpr bool query_smem(int hd, int nt) { return nt > 1 || hd == 64; }
 // A stage: K rows, V rows, a K and a V scale for each 16 positions.
 __host__ __device__ constexpr int stage_bytes(int hd) { return 2 * tile_len(hd) * hd + 32; }
-__host__ __device__ constexpr int ring_bytes(int hd, int nt) { return kWarps * stages(nt) * stage_bytes(hd); }
+__host__ __device__ constexpr int ring_bytes(int hd) { return kWarps * kStages * stage_bytes(hd); }
 // The warps' O at a unit's end, in two halves where a whole one is too large.
 __host__ __device__ constexpr int halves(int hd, int nt) { return hd * nt > 256 ? 2 : 1; }
 __host__ __device__ constexpr int state_bytes(int hd, int nt) { return kWarps * 8 * nt * (hd / halves(hd, nt)) * 4; }
 __host__ __device__ constexpr int query_bytes(int hd, int nt) { return query_smem(hd, nt) ? nt * (hd / 16) * 32 * 8 : 0; }
-__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd, nt) + state_bytes(hd, nt) + query_bytes(hd, nt); }
+__host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd) + state_bytes(hd, nt) + query_bytes(hd, nt); }
 // The reference that a row's weights are taken against, exp2(x - m), follows
 // its scores' maximum only when that is ahead by more than kLag: weights up to
 // 2^kLag are as good in fp16 and fp32, and a tile that raises no maximum needs
@@ -285,7 +294,7 @@ struct Segment {
 // no second kernel.
 template <int FMT, int HD, int NT, int GS, bool LO, bool CL>
 __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(const __grid_constant__ Kv8AttnArgs a, int by_unit) {
-  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = stages(NT), SB = stage_bytes(HD);
+  constexpr int KS = HD / 16, MD = HD / 16, ROWS = 8 * NT, ST = kStages, SB = stage_bytes(HD);
   constexpr int TL = tile_len(HD), TM = TL / 16, NG = TM / GS;
   constexpr bool QS = query_smem(HD, NT);
   extern __shared__ __align__(128) unsigned char sm[];
@@ -430,8 +439,8 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   constexpr int CH = HD / 16, NC = TL * CH / 32;  // 16-byte chunks of a row, copies of a lane and tile
   const unsigned ring = (unsigned)__cvta_generic_to_shared(sm) + warp * ST * SB;
   const unsigned char *ringp = sm + warp * ST * SB;
-  float *so = reinterpret_cast<float *>(sm + ring_bytes(HD, NT));
-  uint2 *sq = reinterpret_cast<uint2 *>(sm + ring_bytes(HD, NT) + state_bytes(HD, NT));
+  float *so = reinterpret_cast<float *>(sm + ring_bytes(HD));
+  uint2 *sq = reinterpret_cast<uint2 *>(sm + ring_bytes(HD) + state_bytes(HD, NT));
   const unsigned ko = k_off<HD>(lane / CH, lane % CH), vo = v_off<HD>(lane / CH, lane % CH);
 
   // A warp's tiles run through the segments in order: index i of the current
@@ -875,6 +884,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         }
       }
     }
+    static_assert(slot_floats(HD, NT) * 4 <= ring_bytes(HD), "a cluster block's state fits the rings");
     const bool whole = !CL && cur.t0 == 0 && cur.t1 == cur.tiles;
     float *slotp = slots + (first ? 0 : slot_floats(HD, NT));
     if (!CL && tid == 0 && cur.t0 == 0 && (by_unit || !whole)) {  // the unit begins here; cut: it goes on in the next piece
