@@ -36,7 +36,7 @@
 // (a kernel that only reads the same bytes through the same rings takes 41
 // us; the joining kernel is 3 to 4 of the difference); 64 ragged rows of the
 // 1B shape: 55 us = 5.6 TB/s.  With 24 query rows per KV head instruction
-// issue bounds it (about 1250 a tile, 34% of cycles): 54 us for 149 MB.
+// issue bounds it (about 1200 a tile, 35% of cycles): 52 us for 149 MB.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -56,8 +56,10 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMinTiles = kWarps;
 // What beginning a unit costs a block, in tiles (its queries' operands, the
 // join of the warps): the line counts it, where pieces are long enough.
-constexpr int kUnitTiles = 8;
-
+// Measured with 0 / 4 / 8 / 12 / 16: 131K positions 55.6 / 48.5 / 47.5 / 48.2 /
+// 49.1 us (one column of rows); 24 rows 78 / 56.4 / 53.1 / 51.6 / 53.6, 16 rows
+// - / 45.3 / 41.2 / 38.8 / 38.1.
+__host__ __device__ constexpr int unit_tiles(int nt) { return nt == 1 ? 8 : 12; }
 // Blocks per SM, as many as the registers leave room for; tiles of a warp's
 // ring (K and V have their own slots: with one tile a half of it is on its way
 // while the other is worked on); query operands in shared memory or in
@@ -358,7 +360,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         all_units += s_units[w];
       }
     }
-    extra = all_tiles >= (int64_t)gridDim.x * 2 * kWarps ? kUnitTiles : 0;
+    extra = all_tiles >= (int64_t)gridDim.x * 2 * kWarps ? unit_tiles(NT) : 0;
     total = all_tiles + extra * all_units;
     piece = (total + gridDim.x - 1) / gridDim.x;
     if (piece < kMinTiles && all_units) piece = max(piece, min((int64_t)kMinTiles, (all_tiles + all_units - 1) / all_units));
@@ -790,7 +792,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       // ---- O^T += vs (V^T P^T)
       // (words of a V row that a thread takes: all at once, or where registers
       // are short a pair at a time)
-      constexpr int VP = HD == 128 && NT == 3 ? 2 : 1, VW = HD / 32 / VP;
+      constexpr int VP = HD == 128 && NT >= 2 ? 2 : 1, VW = HD / 32 / VP;
 #pragma unroll
       for (int vp = 0; vp < VP; ++vp) {
       uint32_t vw[TM][2][2][VW];  // [k-step][8 positions][position][word]
