@@ -266,6 +266,33 @@ def test_read_rounds_once_and_saturates(act):
     assert np.array_equal(f64(only)[0], val)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (16, 8), (24, 16)])
+def test_read_into_strided_outputs(dtype, pad, shift):
+    """Rows on 16-byte and on 32-byte boundaries, heads outside tokens, ragged
+    counts, a head count that does not fill a block's threads; nothing else is
+    touched."""
+    B, Hkv, hd, T, block = 2, 5, 128, 37, 32
+    c = Cache(B, Hkv, hd, 64, block, 1, 1)
+    k, v = data(51, B, 40, Hkv, hd, 1), data(52, B, 40, Hkv, hd, 1)
+    c.append(k, v, [0] * B)
+    pos, count = [3, 11], [T, 20]
+    p, n = (torch.tensor(x, dtype=torch.int32).cuda() for x in (pos, count))
+    big = [torch.full((B, Hkv, T, hd + pad + shift), 7.0, dtype=dtype).cuda() for _ in range(2)]
+    out = [x[..., shift:shift + hd].transpose(1, 2) for x in big]
+    rv.kv8_read(c.c, rv.heads(out[0]), rv.heads(out[1]), B, T, p.data_ptr(), n.data_ptr(), c.err.data_ptr())
+    torch.cuda.synchronize()
+    top = torch.finfo(dtype).max
+    for x, full, src in zip(out, big, (k, v)):
+        for b in range(B):
+            ref = torch.from_numpy(expect(c, f64(src)[b], 40)[0][pos[b]:pos[b] + count[b]]).clamp(-top, top).to(dtype)
+            assert torch.equal(x[b, :count[b]].cpu(), ref)
+            assert (x[b, count[b]:] == 7.0).all()
+        full[..., shift:shift + hd] = 7.0
+        assert (full == 7.0).all()
+    assert int(c.err) == 0
+
+
 # ------------------------------------------------------------------ attention
 
 def check_attention(c, kk, vv, q, scale, pos, count, out, lse):
