@@ -305,7 +305,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
   __shared__ int s_row;
   pdl_wait();
-  pdl_trigger();  // after the wait: the joining kernel may read d_count at once
   const Kv8 &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int grp = a.H / c.Hkv, groups = (a.T * grp + ROWS - 1) / ROWS;
@@ -869,6 +868,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
     }
 
     // ---- join the warps' states
+    if (!more) pdl_trigger();  // the next kernel's blocks come up while the last states are joined
     if (CL) cp_wait<0>();
     __syncthreads();  // the states of the segment before have been read
 #pragma unroll
