@@ -191,7 +191,7 @@ int rv_debug_dump(rv_model *m, int what, void *dst, size_t bytes);
  * one is allocated before the old one is freed, and where that fails
  * (RV_ENOMEM) nothing changes.  The 8-bit caches run on the chain engine
  * (RV_ESTATE with the persistent one, either way round) and need rope_theta
- * above 1.  RV_DUMP_KV then gives the cache's values rounded to act_dtype,
+ * above 1 or rv_set_rope's frequencies.  RV_DUMP_KV then gives the cache's values rounded to act_dtype,
  * and the sentinel at positions that are not cached. */
 #define RV_OPT_KV_CACHE 3
 #define RV_KV_16BIT 0
@@ -459,7 +459,8 @@ size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads
 /* Rotary frequencies of a loaded model for contexts longer than its own
  * (rv_rope_config above): cfg's head_dim must be the model's, rotary_dim the
  * whole head and the layout RV_ROPE_HALF (RV_EINVAL otherwise).  NULL: back to
- * the plain frequencies of rope_theta.  Forgets every cached position, whose
+ * the plain frequencies of rope_theta (RV_ESTATE where the model's cache has 8
+ * bits and rope_theta is not above 1).  Forgets every cached position, whose
  * keys were turned by the old ones.  Prefill, decode steps and the persistent
  * engine all follow. */
 int rv_set_rope(rv_model *m, const rv_rope_config *cfg);

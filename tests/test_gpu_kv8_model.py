@@ -251,3 +251,26 @@ def test_scaled_rotary_frequencies(kind, scaling):
             m.set_rope(c)
         assert e.value.code == rv.RV_EINVAL
     m.close()
+
+
+def test_plain_frequencies_that_the_8bit_cache_lacks():
+    """rope_theta 1 has no plan: the 8-bit cache works on frequencies that were set, and they cannot be taken away."""
+    shape = synth.ModelShape("kv8-theta1", 2, 256, 4, 2, 64, 256, 512, 0, synth.BF16, 1e-5, 1.0)
+    m = rv.Model(shape, synth.make_weights(shape), 2, 64)
+    with pytest.raises(rv.RVError) as e:
+        m.set_kv_cache(rv.KV_INT8)
+    assert e.value.code == rv.RV_EINVAL
+    cfg = rv.RopeConfig(64, 64, rv.ROPE_HALF, rv.ROPE_PLAIN, 0, 10000.0, 0.0, 0.0, 0.0, 0.0, 0.0, 0.0)
+    m.set_rope(cfg)
+    m.set_kv_cache(rv.KV_INT8)
+    L, prompt = shape.n_layers, synth.make_prompt(shape.vocab, 2, 5)
+    m.prefill(prompt, 0.9, L)
+    with pytest.raises(rv.RVError) as e:
+        m.set_rope(None)
+    assert e.value.code == rv.RV_ESTATE
+    assert list(m.dump(rv.DUMP_LENS)[:2]) == [5, 5]  # nothing changed
+    m.decode_step(prompt[:, 0], 0.9, [L, L])
+    m.set_kv_cache(rv.KV_16BIT)
+    m.set_rope(None)
+    m.prefill(prompt, 0.9, L)
+    m.close()

@@ -1177,7 +1177,7 @@ static int set_kv_mode(rv_model *m, int mode) {
   if (mode == m->kv_mode) return RV_OK;
   if (mode && m->engine == RV_ENGINE_PERSISTENT) return fail(RV_ESTATE, "the persistent decode kernel reads the 16-bit cache");
   if (mode && m->Hkv > 1024) return fail(RV_EINVAL, "the 8-bit caches hold up to 1024 KV heads");
-  if (mode && !m->rope.rotary_dim) return fail(RV_EINVAL, "the 8-bit caches need rope_theta above 1");
+  if (mode && !m->rope.rotary_dim) return fail(RV_EINVAL, "the 8-bit caches need rope_theta above 1, or rv_set_rope first");
   RV_CK(cudaStreamSynchronize(m->stream));
   std::vector<void *> fresh;
   Kv8 c{};
@@ -1421,6 +1421,8 @@ int rv_set_rope(rv_model *m, const rv_rope_config *cfg) {
     if (cfg->layout != RV_ROPE_HALF) return fail(RV_EINVAL, "the model's heads are in the half layout");
     int rc = rv_rope_init(cfg, &plan);
     if (rc) return rc;
+  } else if (m->kv_mode && !((double)m->c.rope_theta > 1.0)) {
+    return fail(RV_ESTATE, "the 8-bit caches need rope_theta above 1: a configuration, or the 16-bit cache first");
   }
   RV_CK(cudaStreamSynchronize(m->stream));
   if (cfg) {
