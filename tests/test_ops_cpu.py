@@ -203,3 +203,9 @@ def test_model_calls_reject_a_null_handle():
     assert lib.rv_set_rope(None, C.byref(rv.RopeConfig())) == rv.RV_EINVAL
     assert lib.rv_set_option(None, rv.OPT_KV_CACHE, rv.KV_INT8) == rv.RV_EINVAL
     assert lib.rv_kv_cache_bytes(None) == 0
+
+
+@pytest.mark.parametrize("factor", [1e39, math.inf])
+def test_attention_factor_beyond_fp32_is_refused(factor):
+    refused(rv.rope_plan, 64, attention_factor=factor)
+    assert rv.rope_plan(64, attention_factor=3e38).attention_factor == np.float32(3e38)

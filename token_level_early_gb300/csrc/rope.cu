@@ -325,6 +325,7 @@ extern "C" int rv_rope_init(const rv_rope_config *cfg, rv_rope_plan *plan) {
   p.layout = c.layout;
   double att = c.attention_factor;
   if (att == 0.0) att = c.scaling == RV_ROPE_RAMP && c.factor > 1.0 ? 0.1 * log(c.factor) + 1.0 : 1.0;
+  if (!(att <= 3.402823466e38)) return op_fail(RV_EINVAL, "attention_factor is out of fp32's range");
   p.attention_factor = (float)att;
   const double base = c.scaling == RV_ROPE_BASE ? c.theta * pow(c.factor, r / (r - 2.0)) : c.theta;
   if (!(base > 0.0) || !isfinite(base)) return op_fail(RV_EINVAL, "factor moves theta out of range");
