@@ -477,7 +477,8 @@ int ensure_ws(rv_model *m, long rows) {
 }
 
 // One decoder layer over all rows of the general path; rows are split by
-// route into two lists and each projection runs once per path.
+// route into two lists and each projection runs once per path.  base: the
+// positions of a decode step's tokens, or NULL for a prefill.
 int enqueue_layer_rows(rv_model *m, int l, int B, int T, const int32_t *base, cudaStream_t s) {
   const LayerDev &ly = m->layers[l];
   const long M = (long)B * T;
@@ -485,13 +486,14 @@ int enqueue_layer_rows(rv_model *m, int l, int B, int T, const int32_t *base, cu
   const int32_t *cnt[2] = {m->d_counts, m->d_counts + 1};
   const int act = m->act, d = m->d;
   const int npath = m->has_river ? 2 : 1;
+  const bool step = base != nullptr;  // a decode step (T = 1); without it a prefill of T >= 1 tokens from position 0
   RV_CK(launch_copy_rows(m->gH, d, m->gHin, d, d, (int)M, s));  // a kernel, so the layer's launches chain by PDL
   RV_CK(launch_route_lists(m->st.route, B, T, m->gLists, (int)M, m->d_counts, s));
   // attention sub-block
   RV_CK(launch_rmsnorm_rows(m->gH, ly.attn_norm, d, m->c.rms_eps, act, m->gX, nullptr, m->d_nrows, (int)M, s));
   for (int p = 0; p < npath; ++p)
     if (p == 1 || ly.w[MAT_QKV]) RV_CK(gemm_rows(m, make_mat(m, ly, MAT_QKV), p, m->gX, m->gY, lists[p], cnt[p], (int)M, s));
-  if (m->kv_mode && T == 1) {
+  if (m->kv_mode && step) {
     // one token per row: q and k turned as they stand in Y, K/V quantised from
     // there, attention over the 8-bit cache
     const int64_t ld = m->qkv_n, hd = m->hd;
@@ -515,7 +517,7 @@ int enqueue_layer_rows(rv_model *m, int l, int B, int T, const int32_t *base, cu
     ra.Y = m->gY; ra.q = m->gQ; ra.rope_cs = m->rope_cs; ra.list = nullptr; ra.count = m->d_nrows;
     ra.tokens_per_row = T; ra.base = base;
     RV_CK(launch_rope_rows(ra, (int)M, s));
-    if (T == 1) {
+    if (step) {
       AttnArgs at{};
       at.kv = kv; at.layer = kl; at.H = m->H; at.Hkv = m->Hkv; at.hd = m->hd; at.act = act;
       at.q = m->gQ; at.o = m->gO; at.len = base;
