@@ -1,0 +1,60 @@
+"""The cache attention at the ends of its types' ranges: large scores, queries,
+keys and values that are finite, weights far below the largest.
+
+With one position's score far above all others the definition's result is that
+position's value, however large the scores: its weight is the only one above
+zero, so the output may be off by the weight's rounding to fp16 (2^-11), the
+fp32 steps and the 2^-20 of the block's largest value that kv8_util derives for
+the codes' bias, and the output's own half step."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import token_level_early_gb300 as rv
+from kv8_util import U, attention
+from test_gpu_kv8 import ACT, Cache, check_attention, data, expect, f64, room  # noqa: F401 (room is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def one_hot(seed, n, hd, act, fmt, block, qmag, kmag, room, vmag=1.0, win=None, dtype=None):
+    """Two KV heads with a query head each: (cache, q, k values, v values, the winning position of each head)."""
+    g = torch.Generator().manual_seed(seed)
+    Hkv = 2
+    q = torch.sign(torch.randn(1, 1, Hkv, hd, generator=g)) * (1 + 0.9 * torch.rand(1, 1, Hkv, hd, generator=g)) * qmag
+    k = torch.randn(1, n, Hkv, hd, generator=g).clamp(-1, 1) * 0.25 * kmag
+    v = torch.randn(1, n, Hkv, hd, generator=g).clamp(-1, 1) * vmag
+    win = [n // 3, n - 1] if win is None else win
+    for h in range(Hkv):
+        k[0, win[h], h] = torch.sign(q[0, 0, h]) * kmag
+    q, k, v = (x.to(ACT[act]).cuda() for x in (q, k, v))
+    c = Cache(1, Hkv, hd, max(n, room), block, fmt, act)
+    c.append(k, v, [0])
+    return c, q, expect(c, f64(k)[0], n)[0], expect(c, f64(v)[0], n)[0], win
+
+
+def check_one_hot(c, q, kk, vv, win, out, lse, scale=1.0):
+    name = str(out.dtype).split(".")[1]
+    for h, p in enumerate(win):
+        z = scale * (kk[:, h] @ f64(q)[0, 0, h])
+        d = abs(scale) * 2.0 * np.abs(kk[:, h]).max() * np.abs(f64(q)[0, 0, h]).sum()
+        rest = np.delete(z, p).max()
+        assert z[p] - rest > 0.2 * d > 1000.0          # 2^-19 d is what a score may be off by
+        blk = vv[p // c.block * c.block:(p // c.block + 1) * c.block, h]
+        tol = (2.0 ** -11 + 2.0 ** -12 + U[name]) * np.abs(vv[p, h]) + 2.0 ** -20 * np.abs(blk).max()
+        err = np.abs(f64(out)[0, 0, h] - vv[p, h])
+        assert (err <= tol).all(), (h, float((err / np.maximum(tol, 1e-300)).max()))
+        assert abs(float(lse[0, 0, h]) - z[p]) <= 2.0 ** -19 * d
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("act,qmag,kmag", [(0, 2.0 ** 10, 2.0 ** 10), (0, 30000.0, 30000.0), (1, 2.0 ** 11, 2.0 ** 11), (1, 2.0 ** 15, 2.0 ** 12),
+                                           (1, 2.0 ** 15, 2.0 ** 15), (1, 2.0 ** 40, 2.0 ** 15), (1, 2.0 ** 20, 2.0 ** 60)])
+def test_attention_large_scores(act, qmag, kmag, hd, fmt, room):
+    """Scores from 2^26 to 2^86: their fp32 steps are larger than the softmax's whole range."""
+    c, q, kk, vv, win = one_hot(1, 300, hd, act, fmt, 32, qmag, kmag, room)
+    out, lse = c.attention(q, 1.0, [299])
+    check_one_hot(c, q, kk, vv, win, out, lse)

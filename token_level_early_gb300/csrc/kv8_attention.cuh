@@ -644,6 +644,12 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       // are not negative, so a block's maximum is its scores' times the factor
       // (the loops of one or no turn keep the masks a branch: as predicated
       // operations they would cost every tile)
+      // The scaled score is rounded before the reference is taken off: the
+      // reference is such a rounded score itself, and a fused product minus it
+      // would leave up to half a step of the score, which from 2^28 on is more
+      // than an fp16 weight's range.  __fmul_rn, because a packed product
+      // before a packed sum is fused all the same (24 rows 51.5 -> 52.0 us,
+      // 1K positions 5.8 -> 5.9; the long cases do not change).
       const int edge = p0 + TL > see_all;
       uint32_t pb[TM][NT][2], pl[TM][NT][2];
       float top[NT][2];
@@ -675,7 +681,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
             top[nt][k] = fmaxf(top[nt][k], y * (ks[g] * (k ? rr.y : rr.x)));
           }
-          ahead |= top[nt][k] > m[nt][k] + kLag;
+          ahead |= top[nt][k] - m[nt][k] > kLag;  // (the difference, which is exact where it decides)
         }
       }
       if (__any_sync(0xffffffffu, ahead)) {
@@ -707,10 +713,10 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         const F2 neg = f2(-m[nt][0], -m[nt][1]);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const F2 ff = f2_mul(f2(ks[i / GS], ks[i / GS]), f2(rr.x, rr.y));
+          const float2 ff = make_float2(__fmul_rn(ks[i / GS], rr.x), __fmul_rn(ks[i / GS], rr.y));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            const float2 x = f2_split(f2_fma(f2(s[i][nt][2 * q], s[i][nt][2 * q + 1]), ff, neg));
+            const float2 x = f2_split(f2_add(f2(__fmul_rn(s[i][nt][2 * q], ff.x), __fmul_rn(s[i][nt][2 * q + 1], ff.y)), neg));
             s[i][nt][2 * q] = ex2(x.x);
             s[i][nt][2 * q + 1] = ex2(x.y);
           }

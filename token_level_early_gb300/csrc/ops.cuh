@@ -43,7 +43,8 @@ __device__ __forceinline__ uint32_t pack_act2(float lo, float hi, int act) {
   return r;
 }
 
-// Two fp32 operations in one instruction (each half rounded as the scalar one).
+// Two fp32 operations in one instruction (each half rounded as the scalar one;
+// the compiler may fuse f2_mul into an f2_add of its result).
 struct F2 {
   unsigned long long v;
 };
