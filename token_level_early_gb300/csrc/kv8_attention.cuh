@@ -5,9 +5,9 @@
 // fp32, exponents in base 2).  k_p = s_block x code, so a score is
 // (s_block scale) (q.code): codes go to the tensor pipe as exact fp16 values
 // and the block's scale multiplies the fp32 scores; the V scale multiplies
-// the block's fp32 partial product.  A query row is divided by a power of two
-// (its largest magnitude's), so bf16 rows fit fp16's range; the power returns
-// with the scale.
+// the block's fp32 partial product.  A query row is scaled by a power of two
+// (from its largest magnitude), so bf16 rows fit fp16's range; the power
+// returns with the scale.
 //
 // The products are taken transposed: S^T = K Q^T (16 positions x 8 query rows
 // per mma.m16n8k16), O^T = V^T P^T (16 elements x 8 rows).  With 4 to 8 query
@@ -127,10 +127,24 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { r
 // 4 codes of a word as two fp16 pairs, exact; int8 in units of 2^-24 and
 // biased: byte ^ 0x80 = code + 128 under a zero exponent is the subnormal
 // (code + 128) 2^-24, which costs no conversion.  The products' sums begin at
-// -128 2^-24 x the other operand's sum, and 2^24 joins the scale.  K takes
+// -128 2^-24 x the other operand's sum, and the scales' factors make up for 2^24.  K takes
 // bytes 0, 2 and 1, 3 (the order of the head elements is free).
 template <int FMT>
 __device__ __forceinline__ float code_unit() { return FMT == RV_KV8_INT8 ? 0x1p24f : 1.f; }
+// No factor of a score passes fp32's range before the score does.  Query rows
+// stand at 2^15 (int8: the top of fp16's range) or 2^4 instead of 2^0, which
+// keeps the row's factor, with int8 2^12 of K's 2^24 in it, finite for every
+// |scale q| below 2^130; the other 2^12 meets the product of the block's scale
+// and the row's factor.
+template <int FMT>
+constexpr int kQueryExp = FMT == RV_KV8_INT8 ? 15 : 4;
+template <int FMT>
+constexpr int kRowExp = FMT == RV_KV8_INT8 ? 12 : 0;
+template <int FMT>
+__device__ __forceinline__ float score_factor(float key_scale, float row) {
+  const float f = __fmul_rn(key_scale, row);
+  return FMT == RV_KV8_INT8 ? f * 0x1p12f : f;
+}
 constexpr float kBias = 128.f * 0x1p-24f;
 // (x & mask) ^ flip in one operation: both constants in registers.
 struct I8Const {
@@ -538,10 +552,11 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         for (int i = 0; i < HD / 4; ++i) mx = fmaxf(mx, fabsf(x[i]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        int e = (int)(__float_as_uint(mx) >> 23) - 127;
-        e = min(max(e, -126), 126);
-        const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);  // the scale's sign goes to the query
-        up = __uint_as_float((uint32_t)(127 + e) << 23) * (fabsf(a.scale) * kLog2e * code_unit<FMT>());
+        int e = min((int)(__float_as_uint(mx) >> 23), 254) - 127;
+        constexpr int QE = kQueryExp<FMT>, RE = kRowExp<FMT>;  // both exponents below stay those of normal numbers
+        e = max(e, QE - 126);
+        const float down = copysignf(__uint_as_float((uint32_t)(127 + QE - e) << 23), a.scale);  // the scale's sign goes to the query
+        up = __uint_as_float((uint32_t)(127 + e - QE + RE) << 23) * (fabsf(a.scale) * kLog2e);
 #pragma unroll
         for (int j = 0; j < HD / 64; ++j)
 #pragma unroll
@@ -679,7 +694,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
             for (int i = 1; i < GS; ++i) y = max3(y, s[g * GS + i][nt][k], s[g * GS + i][nt][2 + k]);
             // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
-            top[nt][k] = fmaxf(top[nt][k], y * (ks[g] * (k ? rr.y : rr.x)));
+            top[nt][k] = fmaxf(top[nt][k], y * score_factor<FMT>(ks[g], k ? rr.y : rr.x));
           }
           ahead |= top[nt][k] - m[nt][k] > kLag;  // (the difference, which is exact where it decides)
         }
@@ -713,7 +728,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         const F2 neg = f2(-m[nt][0], -m[nt][1]);
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-          const float2 ff = make_float2(__fmul_rn(ks[i / GS], rr.x), __fmul_rn(ks[i / GS], rr.y));
+          const float2 ff = make_float2(score_factor<FMT>(ks[i / GS], rr.x), score_factor<FMT>(ks[i / GS], rr.y));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const float2 x = f2_split(f2_add(f2(__fmul_rn(s[i][nt][2 * q], ff.x), __fmul_rn(s[i][nt][2 * q + 1], ff.y)), neg));
