@@ -68,3 +68,46 @@ def test_attention_queries_and_keys_over_the_whole_range(qmag, kmag, scale, fmt,
     c, q, kk, vv, win = one_hot(2, 200, 128, 1, fmt, 64, qmag, kmag, room)
     out, lse = c.attention(q, scale, [199])
     check_one_hot(c, q, kk, vv, win, out, lse, scale)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("top", [2.0 ** 112, 2.0 ** 120, 3.0e38])
+def test_attention_values_near_the_end_of_the_range(top, hd, fmt, room):
+    """A block of very large V that has no weight, one that has all of it, and equal weights over many."""
+    c, q, kk, vv, win = one_hot(3, 300, hd, 1, fmt, 32, 64.0, 64.0, room, win=[100, 120])
+    v = torch.from_numpy(vv)[None].clone()
+    v[0, 160:224] *= top                                # values are within 1 here: blocks without weight
+    v[0, 96:128, 1] *= top                              # head 1's winner
+    v = v.to(torch.bfloat16).cuda()
+    k = torch.from_numpy(kk)[None].to(torch.bfloat16).cuda()
+    c = Cache(1, 2, hd, max(300, room), 32, fmt, 1)
+    c.append(k, v, [0])
+    kk, vv = expect(c, f64(k)[0], 300)[0], expect(c, f64(v)[0], 300)[0]
+    for dtype in (torch.bfloat16, torch.float32):
+        out, lse = c.attention(q, 1.0, [299], out=torch.full(q.shape, 7.0, dtype=dtype).cuda())
+        check_one_hot(c, q, kk, vv, win, out, lse)
+    # equal weights: the sum of 3000 values passes fp32, their mean does not
+    v = (data(4, 1, 3000, 1, hd, 1, False).abs().clamp(0.25, 1.0).double() * top).to(torch.bfloat16)
+    c = Cache(1, 1, hd, max(3000, room), 32, fmt, 1)
+    c.append(torch.zeros_like(v), v, [0])
+    vv = expect(c, f64(v)[0], 3000)[0]
+    q = data(5, 1, 1, 4, hd, 1, False)
+    out, lse = c.attention(q, 1.0, [2999])
+    check_attention(c, [np.zeros_like(vv)], [vv], q, 1.0, [2999], None, out, lse)
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_values_near_zero(hd, fmt, room):
+    """V around the smallest scale, 2^-100: relative errors stay what they are elsewhere."""
+    k, v = data(6, 1, 400, 2, hd, 1, False), data(7, 1, 400, 2, hd, 1, False) * 2.0 ** -96
+    c = Cache(1, 2, hd, max(400, room), 64, fmt, 1)
+    c.append(k, v, [0])
+    kk, vv = expect(c, f64(k)[0], 400)[0], expect(c, f64(v)[0], 400)[0]
+    q = data(8, 1, 1, 4, hd, 1, False)
+    out, lse = c.attention(q, 0.1, [399], out=torch.full(q.shape, 7.0, dtype=torch.float32).cuda())
+    up = [x * 2.0 ** 96 for x in (vv, f64(out))]         # by a power of two, so that the bound's absolute part means nothing
+    for h in range(4):
+        ref, rl, D, bound = attention(f64(q)[0, 0, h], kk[:, h // 2], up[0][:, h // 2], 0.1, 400, 64)
+        assert (np.abs(up[1][0, 0, h] - ref) <= bound("float32")).all()

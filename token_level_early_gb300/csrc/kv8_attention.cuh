@@ -129,8 +129,13 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { r
 // (code + 128) 2^-24, which costs no conversion.  The products' sums begin at
 // -128 2^-24 x the other operand's sum, and the scales' factors make up for 2^24.  K takes
 // bytes 0, 2 and 1, 3 (the order of the head elements is free).
+// The running O is kept in units of 2^40: a sum of 2^24 weights of up to 2^15
+// times values at the end of bf16's range stays finite, and at V scales of
+// 2^-100, the smallest, fp32's subnormals still hold 16 bits of a block's largest.  int8
+// products come 2^24 of it too small already.
 template <int FMT>
-__device__ __forceinline__ float code_unit() { return FMT == RV_KV8_INT8 ? 0x1p24f : 1.f; }
+constexpr float kValueUnit = FMT == RV_KV8_INT8 ? 0x1p-16f : 0x1p-40f;
+constexpr float kOutUnit = 0x1p40f;
 // No factor of a score passes fp32's range before the score does.  Query rows
 // stand at 2^15 (int8: the top of fp16's range) or 2^4 instead of 2^0, which
 // keeps the row's factor, with int8 2^12 of K's 2^24 in it, finite for every
@@ -276,10 +281,10 @@ __device__ __forceinline__ float4 ld_cluster4(unsigned at, int k) {
   return x;
 }
 
-// 4 elements of an output row from its joined state (x = weighted sum, mm =
-// maximum in base 2, ll = sum).
+// 4 elements of an output row from its joined state (x = weighted sum in units
+// of kOutUnit, mm = reference in base 2, ll = sum).
 __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, int h, int d, float4 x, float mm, float ll) {
-  const float f = ll == 0.f ? 0.f : 1.f / ll;  // nothing seen: zeros
+  const float f = ll == 0.f ? 0.f : kOutUnit / ll;  // nothing seen: zeros
   x.x *= f; x.y *= f; x.z *= f; x.w *= f;
   const int act = a.c.act;
   const int64_t o = b * a.out.sb + t * a.out.st + h * a.out.sh + d;
@@ -770,7 +775,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float x = fs[TM + i * GS] * code_unit<FMT>();
+          const float x = fs[TM + i * GS] * kValueUnit<FMT>;
           vs[i][nt] = f2(x, x);
         }
 #pragma unroll 1
