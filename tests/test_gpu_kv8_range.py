@@ -111,3 +111,48 @@ def test_attention_values_near_zero(hd, fmt, room):
     for h in range(4):
         ref, rl, D, bound = attention(f64(q)[0, 0, h], kk[:, h // 2], up[0][:, h // 2], 0.1, 400, 64)
         assert (np.abs(up[1][0, 0, h] - ref) <= bound("float32")).all()
+
+
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("n,gap,quiet", [(30, 20.0, 1), (30, 24.0, 1), (30, 27.0, 1), (3000, 22.0, 1), (3000, 24.0, 1), (3000, 23.4, 64), (3000, 25.5, 64)])
+def test_attention_first_token_that_takes_nearly_all(n, gap, quiet, hd, fmt, act, room):
+    """A first token with 2^gap times the weight of each of the others, and V =
+    0 in the first `quiet` tokens, so that the others make the output: their
+    weights keep their bits far below the largest one's.  A weight w of a row
+    whose largest is 1 is off by 2^-32 at most besides its relative rounding
+    (fp16's smallest step is 2^-24, half of it 2^-25, and the largest weights
+    stand at 2^7 or above).  int8 V codes enter the fp32 sums as code + 128,
+    with -128 x the sum of the weights taken off: the first token's product is
+    up to 128 code steps of its weight, the sum that holds it has at most 64
+    products and 8 running sums, and the tensor pipe cuts each off at the last
+    of 24 bits of the largest (it does not say how it rounds): 72 x 2^-23 x 128
+    steps, a step being the block's largest |v| / 127, is below 2^-16 x weight
+    x largest |v|.  Nothing where that block is all zero."""
+    block = 64
+    g = torch.Generator().manual_seed(9)
+    k = torch.zeros(1, n, 1, hd)
+    k[0, 0, 0, 0] = 1.0
+    v = torch.rand(1, n, 1, hd, generator=g) * 0.5 + 0.5
+    v[0, :quiet] = 0.0
+    q = torch.zeros(1, 1, 2, hd)
+    q[..., 0] = gap
+    k, v, q = (x.to(ACT[act]).cuda() for x in (k, v, q))
+    c = Cache(1, 1, hd, max(n, room), block, fmt, act)
+    c.append(k, v, [0])
+    kk, vv = expect(c, f64(k)[0], n)[0][:, 0], expect(c, f64(v)[0], n)[0][:, 0]
+    scale = float(np.float32(math.log(2.0)))
+    out, lse = c.attention(q, scale, [n - 1], out=torch.full(q.shape, 7.0, dtype=torch.float32).cuda())
+    z = scale * (kk @ f64(q)[0, 0, 0])
+    w = np.exp(z - z.max())
+    ref = w @ vv / w.sum()
+    d = scale * gap * 2.0 * np.abs(kk).max()
+    top = np.array([np.abs(vv[i:i + block]).max() for i in range(0, n, block)]).repeat(block)[:n]
+    tol = (2.0 ** -11 + 2.0 ** -12 + 2.0 * 2.0 ** -19 * d + 2.0 ** -23) * ref + n * 2.0 ** -32
+    if fmt == 0:
+        tol = tol + 2.0 ** -16 * (w @ top / w.sum())
+    for h in range(2):
+        err = np.abs(f64(out)[0, 0, h] - ref)
+        assert (err <= tol).all(), (h, float((err / tol).max()), float((err / ref).max()))
+        assert abs(float(lse[0, 0, h]) - (z.max() + math.log(w.sum()))) <= 2.0 ** -19 * d + 2.0 ** -13

@@ -80,12 +80,16 @@ __host__ __device__ constexpr int halves(int hd, int nt) { return hd * nt > 256 
 __host__ __device__ constexpr int state_bytes(int hd, int nt) { return kWarps * 8 * nt * (hd / halves(hd, nt)) * 4; }
 __host__ __device__ constexpr int query_bytes(int hd, int nt) { return query_smem(hd, nt) ? nt * (hd / 16) * 32 * 8 : 0; }
 __host__ __device__ constexpr int smem_bytes(int hd, int nt) { return ring_bytes(hd) + state_bytes(hd, nt) + query_bytes(hd, nt); }
-// The reference that a row's weights are taken against, exp2(x - m), follows
-// its scores' maximum only when that is ahead by more than kLag: weights up to
-// 2^kLag are as good in fp16 and fp32, and a tile that raises no maximum needs
-// no reduction over the warp and no rescaling.  kUnseen: nothing seen yet
-// (finite, so that -m stays an ordinary addend).
-constexpr float kLag = 8.f, kUnseen = -3.402823466e38f;
+// The reference that a row's weights are taken against, exp2(x - m), is set to
+// kTop below its scores' maximum and follows it only when that is ahead by more
+// than kLag: weights up to 2^kLag are as good in fp16 (whose largest value is
+// just below 2^16) and in fp32, and a tile that raises no maximum needs no
+// reduction over the warp and no rescaling.  kTop puts the largest weight at
+// 2^7 or above, so that fp16 holds weights down to 2^-31 of it, and down to
+// 2^-21 with all bits: behind a first token that takes nearly all, as trained
+// models have, the rest still counts.  kUnseen: nothing seen yet (finite, so
+// that -m stays an ordinary addend).
+constexpr float kTop = 7.f, kLag = 15.f, kUnseen = -3.402823466e38f;
 // One cut unit's state: O [rows][hd], then m and l [rows].
 __host__ __device__ constexpr size_t slot_floats(int hd, int nt) { return (size_t)8 * nt * (hd + 2); }
 
@@ -127,8 +131,11 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { r
 // 4 codes of a word as two fp16 pairs, exact; int8 in units of 2^-24 and
 // biased: byte ^ 0x80 = code + 128 under a zero exponent is the subnormal
 // (code + 128) 2^-24, which costs no conversion.  The products' sums begin at
-// -128 2^-24 x the other operand's sum, and the scales' factors make up for 2^24.  K takes
-// bytes 0, 2 and 1, 3 (the order of the head elements is free).
+// -128 2^-24 x the other operand's sum, and the scales' factors make up for
+// 2^24.  What the bias costs: a V sum's terms are cut at the last bit of the
+// largest, 128 code steps of the heaviest weight: seen as up to 2.6 x 2^-20 of
+// the weight x the block's largest |v|.  K takes bytes 0, 2 and 1, 3 (the order
+// of the head elements is free).
 // The running O is kept in units of 2^40: a sum of 2^24 weights of up to 2^15
 // times values at the end of bf16's range stays finite, and at V scales of
 // 2^-100, the smallest, fp32's subnormals still hold 16 bits of a block's largest.  int8
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[nt][k]);
+            x = fmaxf(x - kTop, m[nt][k]);
             al[k] = ex2(m[nt][k] - x);
             m[nt][k] = x;
           }
