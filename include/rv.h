@@ -445,7 +445,8 @@ int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_ou
  * merged.  Scores, softmax and sums are fp32; the probabilities enter the
  * product with V as fp16.  Finite rows give finite results where |scale| x
  * |q| stays below 2^130 and |scale| x |q| x |k| below 2^119 (largest
- * magnitudes of the row and of the blocks it sees): beyond, scores pass fp32.  workspace: rv_kv8_attention_workspace bytes,
+ * magnitudes of the row and of the blocks it sees): beyond, scores pass fp32.
+ * A query row with an infinity or a NaN gives NaN where it sees anything.  workspace: rv_kv8_attention_workspace bytes,
  * 16-byte aligned, no contents needed or kept (short contexts may not use
  * it); calls that may run at the same time (other streams, graphs replayed
  * concurrently) need one each. */

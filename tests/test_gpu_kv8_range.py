@@ -156,3 +156,21 @@ def test_attention_first_token_that_takes_nearly_all(n, gap, quiet, hd, fmt, act
         err = np.abs(f64(out)[0, 0, h] - ref)
         assert (err <= tol).all(), (h, float((err / tol).max()), float((err / ref).max()))
         assert abs(float(lse[0, 0, h]) - (z.max() + math.log(w.sum()))) <= 2.0 ** -19 * d + 2.0 ** -13
+
+
+@pytest.mark.parametrize("fmt", [0, 1])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_attention_query_rows_that_are_not_finite(bad, fmt, room):
+    """An infinity or a NaN in a query row makes that row NaN, whatever the keys' signs, and no other."""
+    hd, n = 64, 100
+    k = -data(11, 1, n, 1, hd, 1, False).abs()
+    v = data(12, 1, n, 1, hd, 1, False)
+    c = Cache(1, 1, hd, max(n, room), 32, fmt, 1)
+    c.append(k, v, [0])
+    q = data(13, 1, 3, 4, hd, 1, False)
+    q[0, 1, 2, 5] = bad
+    out, lse = c.attention(q, 0.125, [n - 3])
+    hit = torch.zeros(1, 3, 4, dtype=torch.bool, device="cuda")
+    hit[0, 1, 2] = True
+    assert torch.isnan(lse[hit]).all() and torch.isnan(out[hit]).all()
+    assert torch.isfinite(lse[~hit]).all() and torch.isfinite(out[~hit]).all()
