@@ -443,7 +443,8 @@ int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_ou
  * receives the natural log of the softmax denominators (-infinity where
  * nothing is seen), with which partial results over several caches can be
  * merged.  Scores, softmax and sums are fp32; the probabilities enter the
- * product with V as fp16.  Finite rows give finite results where |scale| x
+ * product with V as fp16 (fp16 caches and RV_F32 outputs: as two fp16 terms,
+ * 22 bits).  Finite rows give finite results where |scale| x
  * |q| stays below 2^130 and |scale| x |q| x |k| below 2^119 (largest
  * magnitudes of the row and of the blocks it sees): beyond, scores pass fp32.
  * A query row with an infinity or a NaN gives NaN where it sees anything.  workspace: rv_kv8_attention_workspace bytes,

@@ -28,8 +28,8 @@
 // the units that lie in it and leaves the state (m, l, O) of at most two cut
 // ones, which a second kernel, chained by programmatic dependent launch,
 // joins.  Short contexts take a cluster per unit instead, which joins through
-// distributed shared memory.  fp16 caches split each weight into a high and a
-// low fp16 term.
+// distributed shared memory.  fp16 caches and fp32 outputs split each weight
+// into a high and a low fp16 term.
 //
 // Measured on a GB300 (graph of passes, inputs larger than L2): one row of
 // 131,000 positions, 8 KV heads of 128: 47 us = 5.7 TB/s, 85% of a copy's rate
@@ -1151,8 +1151,8 @@ cudaError_t launch_lo(const Kv8AttnArgs &a, int n_sm, cudaStream_t s, int pdl) {
 
 template <int FMT, int HD, int NT>
 cudaError_t launch_nt(const Kv8AttnArgs &a, int n_sm, cudaStream_t s, int pdl) {
-  // fp16 outputs have 11 bits: weights rounded to as many would show in them
-  return a.c.act == RV_F16 ? launch_lo<FMT, HD, NT, true>(a, n_sm, s, pdl) : launch_lo<FMT, HD, NT, false>(a, n_sm, s, pdl);
+  // fp16 outputs have 11 bits and fp32 ones 24: weights rounded to 11 would show in them
+  return a.c.act == RV_F16 || (a.out_dtype == RV_F32 && !a.round_out) ? launch_lo<FMT, HD, NT, true>(a, n_sm, s, pdl) : launch_lo<FMT, HD, NT, false>(a, n_sm, s, pdl);
 }
 
 template <int FMT>
