@@ -253,8 +253,8 @@ __global__ void __launch_bounds__(256) k_read(Kv8 c, Kv8Io io, ReadGrid g) {
     const int64_t p = p0 + k * pass;
     ok[k] = t0 + tl + k * pass < t1 && p >= 0 && p < c.T;
     if (ok[k]) {
-      w[k] = __ldg(reinterpret_cast<const uint4 *>(src + k * pass * HD));
-      s[k] = __ldg(scale + (p >> shift));
+      w[k] = *reinterpret_cast<const uint4 *>(src + k * pass * HD);
+      s[k] = scale[p >> shift];
     }
   }
 #pragma unroll

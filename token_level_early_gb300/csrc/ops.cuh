@@ -14,7 +14,10 @@ namespace rv {
 // Every kernel of these operators waits for its predecessor's end before it
 // touches memory (griddepcontrol.wait), so all of them may be launched with
 // programmatic dependence on whatever is before them in the stream: the
-// launch then overlaps the predecessor's tail.
+// launch then overlaps the predecessor's tail.  So what the predecessor writes
+// is written during their lifetime, and none of them reads memory through the
+// read-only path (__ldg), which holds only for data that no one writes while
+// the kernel lives.
 
 // Records the message and returns the code.
 int op_fail(int code, const char *fmt, ...);
@@ -76,9 +79,9 @@ __device__ __forceinline__ F2 f2_fma(F2 a, F2 b, F2 c) {
 
 // A row's token count and first position (see the conventions in rv.h).
 __device__ __forceinline__ int row_count(const int32_t *count, int b, int T) {
-  return count ? min(max(__ldg(count + b), 0), T) : T;
+  return count ? min(max(count[b], 0), T) : T;
 }
-__device__ __forceinline__ int row_pos(const int32_t *pos, int b) { return pos ? __ldg(pos + b) : 0; }
+__device__ __forceinline__ int row_pos(const int32_t *pos, int b) { return pos ? pos[b] : 0; }
 
 constexpr int kKv8ErrPos = 64;  // bit 6 of *d_err: a position outside the cache
 
