@@ -8,7 +8,7 @@ import token_level_early_gb300 as rv
 CSRC = os.path.join(os.path.dirname(os.path.abspath(rv.__file__)), "csrc")
 
 
-@pytest.mark.parametrize("name", ["ops.cuh", "rope.cu", "kv8.cu", "kv8_attention.cuh", "kv8_attention.cu", "kv8_attention_e4m3.cu"])
+@pytest.mark.parametrize("name", ["ops.cuh", "rope.cu", "kv8.cu", "kv8_attention.cuh", "kv8_attention.cu", "kv8_attention_e4m3.cu", "rows_mma.cu"])
 def test_no_read_only_loads_in_chained_kernels(name):
     """These kernels are launched before their predecessor in the stream has
     ended: the read-only path is for memory that no one writes while a kernel

@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(RW * 32, 2) k_rows_mma(Mat mt, const float *X,
           const int m = rows[ib + u * RPP];
           lo[u] = hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
           if (m >= 0 && full) {
-            lo[u] = __ldg(reinterpret_cast<const float4 *>(X + (size_t)m * K + k));
-            hi[u] = __ldg(reinterpret_cast<const float4 *>(X + (size_t)m * K + k + 4));
+            lo[u] = *reinterpret_cast<const float4 *>(X + (size_t)m * K + k);
+            hi[u] = *reinterpret_cast<const float4 *>(X + (size_t)m * K + k + 4);
           } else if (m >= 0) {
             float x[8];
 #pragma unroll
