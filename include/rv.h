@@ -417,9 +417,11 @@ typedef struct rv_kv8 {
 /* Append B x T tokens' K and V (n_kv_heads heads each; act_dtype, or RV_F32
  * rounded to act_dtype first) at positions d_pos[b].. of rows 0..B-1.  The
  * positions before d_pos[b] must have been appended before.  A row may go
- * back (drafted tokens refused) by at most `block` positions below the
- * highest one written since, and continue from there; what lay behind is
- * forgotten.  Rows of count 0 are left alone.  A row whose d_pos is negative
+ * back and continue from there, what lay behind is forgotten: to any multiple
+ * of `block` (0: it starts over), and elsewhere (drafted tokens refused) to at
+ * most `block` positions below the highest end that the row has reached since
+ * the first token of that block was last written.  Rows of count 0 are left
+ * alone.  A row whose d_pos is negative
  * or at least max_seq is left alone, and tokens at max_seq and beyond are
  * dropped: either sets bit 6 (64) of *d_err (or NULL: not reported). */
 int rv_kv8_append(const rv_kv8 *cache, const rv_heads *k, const rv_heads *v, int B, int T, const int32_t *d_pos,
