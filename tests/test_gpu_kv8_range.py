@@ -62,7 +62,8 @@ def test_attention_large_scores(act, qmag, kmag, hd, fmt, room):
 
 @pytest.mark.parametrize("fmt", [0, 1])
 @pytest.mark.parametrize("qmag,kmag,scale", [(2.0 ** 105, 2.0 ** -92, 1.0), (2.0 ** 126, 2.0 ** -93, 1.0), (2.0 ** 126, 2.0 ** -20, 1.0), (2.0 ** -13, 2.0 ** 126, 1.0),
-                                             (2.0 ** 60, 2.0 ** 50, 1.0), (2.0 ** 110, 1.0, 128 ** -0.5), (2.0 ** -110, 2.0 ** 126, 1.0), (2.0 ** 126, 2.0 ** -93, 4.0)])
+                                             (2.0 ** 60, 2.0 ** 50, 1.0), (2.0 ** 110, 1.0, 128 ** -0.5), (2.0 ** -110, 2.0 ** 126, 1.0), (2.0 ** 126, 2.0 ** -93, 4.0),
+                                             (2.0 ** -120, 0.125, 3.0 * 2.0 ** 126), (2.0 ** 20, 2.0 ** 100, 2.0 ** -100)])
 def test_attention_queries_and_keys_over_the_whole_range(qmag, kmag, scale, fmt, room):
     """bf16 queries and keys anywhere in the type's range, as long as scale x |q| x |k| stays below 2^119."""
     c, q, kk, vv, win = one_hot(2, 200, 128, 1, fmt, 64, qmag, kmag, room)

@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
         constexpr int QE = kQueryExp<FMT>, RE = kRowExp<FMT>;  // both exponents below stay those of normal numbers
         e = max(e, QE - 126);
         const float down = copysignf(__uint_as_float((uint32_t)(127 + QE - e) << 23), a.scale);  // the scale's sign goes to the query
-        up = __uint_as_float((uint32_t)(127 + e - QE + RE) << 23) * (fabsf(a.scale) * kLog2e);
+        up = __uint_as_float((uint32_t)(127 + e - QE + RE) << 23) * fabsf(a.scale) * kLog2e;
         if (mx == INFINITY) up = __int_as_float(0x7fc00000);  // also where all its scores would be -infinity
 #pragma unroll
         for (int j = 0; j < HD / 64; ++j)
