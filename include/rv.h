@@ -186,13 +186,16 @@ int rv_debug_dump(rv_model *m, int what, void *dst, size_t bytes);
  * rv_kv8 cache below, block 64): about half the memory and half the bytes that
  * the decode attention reads.  Decode steps quantise their K/V as they are
  * written and attend over the 8-bit cache; a prefill attends over its own
- * 16-bit K/V and then quantises them.  Setting it to another value forgets
+ * 16-bit K/V and then quantises them.  A step has a kernel a layer more than on
+ * the 16-bit cache, so at short contexts it is the slower one (batch 1 of the
+ * 8B shape: below about 16K positions).  Setting it to another value forgets
  * every cached position (as rv_kv_reset does) and replaces the cache; the new
  * one is allocated before the old one is freed, and where that fails
  * (RV_ENOMEM) nothing changes.  The 8-bit caches run on the chain engine
  * (RV_ESTATE with the persistent one, either way round) and need rope_theta
- * above 1 or rv_set_rope's frequencies.  RV_DUMP_KV then gives the cache's values rounded to act_dtype,
- * and the sentinel at positions that are not cached. */
+ * above 1 or rv_set_rope's frequencies.  RV_DUMP_KV then gives the cache's
+ * values rounded to act_dtype, and the sentinel at positions that are not
+ * cached. */
 #define RV_OPT_KV_CACHE 3
 #define RV_KV_16BIT 0
 #define RV_KV_INT8 1
@@ -449,7 +452,10 @@ int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_ou
  * 22 bits).  Finite rows give finite results where |scale| x
  * |q| stays below 2^130 and |scale| x |q| x |k| below 2^119 (largest
  * magnitudes of the row and of the blocks it sees): beyond, scores pass fp32.
- * A query row with an infinity or a NaN gives NaN where it sees anything.  workspace: rv_kv8_attention_workspace bytes,
+ * A query row with an infinity or a NaN gives NaN where it sees anything.
+ * How the work is cut depends on the shapes and on the cache's max_seq, not on
+ * the rows' lengths: a cache with room for about 4096 positions takes 6 us for
+ * one row of 1024 positions and 8 KV heads, one with room for 131,072 takes 10.  workspace: rv_kv8_attention_workspace bytes,
  * 16-byte aligned, no contents needed or kept (short contexts may not use
  * it); calls that may run at the same time (other streams, graphs replayed
  * concurrently) need one each. */

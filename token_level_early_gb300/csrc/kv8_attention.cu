@@ -30,7 +30,11 @@ cudaError_t launch_int8(const Kv8AttnArgs &a, int nt, int n_sm, cudaStream_t s, 
 // 16.5 / 11.0; 16 such rows: 256: 17.9 / 6.8 / 6.3 / 11.3 / 22, 1024: 11.9 /
 // 11.1 / 9.3 / 13.8 / 23, 2048: 13.6 / 16.8 / 13.5 / 16 / 25, 4096: 20.4 / 30 /
 // 21 / 24 / 33; one KV head: 2048: 7.7 / 17 / 11 / 8.2 / 6.7, 4096: 7.7 / 29 /
-// 17 / 11 / 8.1.
+// 17 / 11 / 8.1.  Where the rule is not the faster one: it leaves clusters of 8
+// for the line above 16 tiles a block, although 8 KV heads at 8192 positions
+// are 1.9 us faster on them, and stays with them for one KV head at 4096, which
+// costs 0.4.  `most` is the cache's max_seq in rv_kv8_attention, which cannot
+// see the rows' lengths on the device, and the longest row in the model.
 int kv8_attention_cluster(const Kv8 &c, int B, int T, int H, int n_sm, int most) {
   const int rows = T * (H / c.Hkv), nt = kv8a::pick_nt(rows);
   const int64_t tiles = (most + kv8a::tile_len(c.hd) - 1) / kv8a::tile_len(c.hd);

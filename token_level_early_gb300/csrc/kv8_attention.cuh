@@ -32,11 +32,15 @@
 // into a high and a low fp16 term.
 //
 // Measured on a GB300 (graph of passes, inputs larger than L2): one row of
-// 131,000 positions, 8 KV heads of 128: 47 us = 5.7 TB/s, 85% of a copy's rate
-// (a kernel that only reads the same bytes through the same rings takes 41
-// us; the joining kernel is 3 to 4 of the difference); 64 ragged rows of the
-// 1B shape: 55 us = 5.6 TB/s.  With 24 query rows per KV head instruction
-// issue bounds it (about 1200 a tile, 35% of cycles): 52 us for 149 MB.
+// 131,000 positions, 8 KV heads of 128: 46.6 us = 5.8 TB/s, 86% of a copy's
+// rate (a kernel that only reads the same bytes through the same rings takes
+// 41 us; the joining kernel is 3 to 4 of the difference); 64 ragged rows of the
+// 1B shape: 54.7 us = 5.7 TB/s.  16 rows of 24 query rows per KV head take 52
+// us for 149 MB, and no unit is full (DRAM 33%, tensor pipe 36%, issue 36%):
+// 255 registers leave two warps per scheduler, and of the 5.5 cycles between a
+// warp's instructions 1.6 go to fixed latencies (products that add to one sum,
+// transposes), 0.8 to instruction fetch, 0.5 to the full tensor pipe's queue
+// and 0.5 to shared and global loads: latency that two warps do not hide.
 #pragma once
 
 #include <cuda_fp8.h>
