@@ -449,16 +449,16 @@ int rv_kv8_read(const rv_kv8 *cache, const rv_heads *k_out, const rv_heads *v_ou
  * nothing is seen), with which partial results over several caches can be
  * merged.  Scores, softmax and sums are fp32; the probabilities enter the
  * product with V as fp16 (fp16 caches and RV_F32 outputs: as two fp16 terms,
- * 22 bits).  Finite rows give finite results where |scale| x
- * |q| stays below 2^130 and |scale| x |q| x |k| below 2^119 (largest
- * magnitudes of the row and of the blocks it sees): beyond, scores pass fp32.
- * A query row with an infinity or a NaN gives NaN where it sees anything.
- * How the work is cut depends on the shapes and on the cache's max_seq, not on
- * the rows' lengths: a cache with room for about 4096 positions takes 6 us for
- * one row of 1024 positions and 8 KV heads, one with room for 131,072 takes 10.  workspace: rv_kv8_attention_workspace bytes,
- * 16-byte aligned, no contents needed or kept (short contexts may not use
- * it); calls that may run at the same time (other streams, graphs replayed
- * concurrently) need one each. */
+ * 22 bits).  Finite rows give finite results where |scale| x |q| stays below
+ * 2^130 and |scale| x |q| x |k| below 2^119 (largest magnitudes of the row and
+ * of the blocks it sees): beyond, scores pass fp32.  A query row with an
+ * infinity or a NaN gives NaN where it sees anything.  How the work is cut
+ * depends on the shapes and on the cache's max_seq, not on the rows' lengths:
+ * a cache with room for up to 4096 positions takes 6 us for one row of 1024
+ * positions and 8 KV heads, one with room for 131,072 takes 10.  workspace:
+ * rv_kv8_attention_workspace bytes, 16-byte aligned, no contents needed or
+ * kept (short contexts may not use it); calls that may run at the same time
+ * (other streams, graphs replayed concurrently) need one each. */
 int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, float scale,
                      const int32_t *d_pos, const int32_t *d_count, float *d_lse, void *workspace,
                      size_t workspace_bytes, void *stream);

@@ -142,8 +142,8 @@ __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { r
 // of the head elements is free).
 // The running O is kept in units of 2^40: a sum of 2^24 weights of up to 2^15
 // times values at the end of bf16's range stays finite, and at V scales of
-// 2^-100, the smallest, fp32's subnormals still hold 16 bits of a block's largest.  int8
-// products come 2^24 of it too small already.
+// 2^-100, the smallest, fp32's subnormals still hold 16 bits of a block's
+// largest.  int8 products come 2^24 of it too small already.
 template <int FMT>
 constexpr float kValueUnit = FMT == RV_KV8_INT8 ? 0x1p-16f : 0x1p-40f;
 constexpr float kOutUnit = 0x1p40f;
@@ -711,7 +711,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
 #pragma unroll
             for (int i = 1; i < GS; ++i) y = max3(y, s[g * GS + i][nt][k], s[g * GS + i][nt][2 + k]);
             // -infinity x 0 of an unseen block: a NaN, which fmaxf passes over
-            top[nt][k] = fmaxf(top[nt][k], y * score_factor<FMT>(ks[g], k ? rr.y : rr.x));
+            top[nt][k] = fmaxf(top[nt][k], __fmul_rn(y, score_factor<FMT>(ks[g], k ? rr.y : rr.x)));
           }
           ahead |= top[nt][k] - m[nt][k] > kLag;  // (the difference, which is exact where it decides)
         }
