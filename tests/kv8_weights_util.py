@@ -13,7 +13,7 @@ def case(seed, H, n, hd):
     return q, k, g.uniform(-1.0, 1.0, (n, hd))
 
 
-def bound(q, k, v, block, fmt, scale=1.0):
+def bound(q, k, v, block, scale=1.0):
     """(out, bound) of one query row over values k, v [n][hd], n <= 40, in 64 bits:
     - a weight is off by 2^-22 in its two terms (2^-11 of what 2^-11 left), by
       2^-22 in the exponential, and by twice its score's 2^-19 x D (kv8_util);
@@ -21,19 +21,17 @@ def bound(q, k, v, block, fmt, scale=1.0):
       bits of the largest, the weights' sum n terms, and the joins of 4 warps
       and 8 blocks, the division and the scaling are below 40 steps: (2 n + n +
       40) x 2^-23 of sum w |v|;
-    - int8: 2^-16 x sum of weight x the block's largest |v| (the codes' bias);
     - the fp32 output's half step."""
     n = k.shape[0]
     assert n <= 40
-    ktop, vtop = (np.array([np.abs(x[i:i + block]).max() for i in range(0, n, block)]).repeat(block)[:n] for x in (k, v))
+    ktop = np.array([np.abs(k[i:i + block]).max() for i in range(0, n, block)]).repeat(block)[:n]
     z = scale * (k @ q)
     d = abs(scale) * float((2.0 * ktop * np.abs(q).sum()).max())
     w = np.exp(z - z.max())
     w /= w.sum()
     rel = 2.0 ** -22 + 2.0 ** -22 + 2.0 * 2.0 ** -19 * d + (3 * n + 40) * 2.0 ** -23
-    off = rel * (w @ np.abs(v)) + (2.0 ** -16 * float(w @ vtop) if fmt == 0 else 0.0)
     out = w @ v
-    return out, off + 2.0 ** -24 * np.abs(out)
+    return out, rel * (w @ np.abs(v)) + 2.0 ** -24 * np.abs(out)
 
 
 def product(q, k, v, terms, scale=1.0):

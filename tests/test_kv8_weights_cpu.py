@@ -14,7 +14,7 @@ def test_bound_tells_one_term_from_two(n, fmt):
     k, v = quantise(k, fmt, 32)[0], quantise(v, fmt, 32)[0]
     worst = {1: 0.0, 2: 0.0, -2: 0.0}
     for row in q:
-        ref, tol = bound(row, k, v, 32, fmt)
+        ref, tol = bound(row, k, v, 32)
         for terms in worst:
             worst[terms] = max(worst[terms], float((np.abs(product(row, k, v, terms) - ref) / tol).max()))
     assert worst[2] < 0.5 and worst[1] > 1.2 and worst[-2] > 1.2, worst

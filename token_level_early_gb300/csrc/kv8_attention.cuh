@@ -35,7 +35,7 @@
 // 131,000 positions, 8 KV heads of 128: 46.6 us = 5.8 TB/s, 86% of a copy's
 // rate (a kernel that only reads the same bytes through the same rings takes
 // 41 us; the joining kernel is 3 to 4 of the difference); 64 ragged rows of the
-// 1B shape: 54.7 us = 5.7 TB/s.  16 rows of 24 query rows per KV head take 52
+// 1B shape: 54.7 us = 5.7 TB/s.  16 rows of 24 query rows per KV head take 50.6
 // us for 149 MB, and no unit is full (DRAM 33%, tensor pipe 36%, issue 36%):
 // 255 registers leave two warps per scheduler, and of the 5.5 cycles between a
 // warp's instructions 1.6 go to fixed latencies (products that add to one sum,
@@ -132,20 +132,25 @@ __device__ __forceinline__ __half2 bits_h2(uint32_t x) { return *reinterpret_cas
 __device__ __forceinline__ uint32_t h2_bits(__half2 x) { return *reinterpret_cast<uint32_t *>(&x); }
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t s) { return __byte_perm(a, b, s); }
 
-// 4 codes of a word as two fp16 pairs, exact; int8 in units of 2^-24 and
+// K: 4 codes of a word as two fp16 pairs, exact; int8 in units of 2^-24 and
 // biased: byte ^ 0x80 = code + 128 under a zero exponent is the subnormal
 // (code + 128) 2^-24, which costs no conversion.  The products' sums begin at
-// -128 2^-24 x the other operand's sum, and the scales' factors make up for
-// 2^24.  What the bias costs: a V sum's terms are cut at the last bit of the
-// largest, 128 code steps of the heaviest weight: seen as up to 2.6 x 2^-20 of
-// the weight x the block's largest |v|.  K takes bytes 0, 2 and 1, 3 (the order
-// of the head elements is free).
+// -128 2^-24 x the query's sum, and the score's factors make up for 2^24.  The
+// tensor pipe cuts a sum's terms at the last bit that the largest exponent
+// leaves them, and a subnormal's exponent is that of 2^-14: a score is off by
+// some 2^-22 of the largest it could be.  K takes bytes 0, 2 and 1, 3 (the
+// order of the head elements is free).
+// V: an output may be much smaller than its block's largest values, and the
+// same cut would show in it (2.5 x 10^-4 of outputs over 75K positions).  So its
+// codes are taken without bias and as normal numbers: byte ^ 0x80 under the
+// exponent of 1024 is 1152 + code, less 1152 by one subtraction a pair (below
+// 2 x 10^-6; 24 rows 52.1 -> 50.6 us, since the products that summed the
+// weights for the bias are gone, 1K positions 5.8 -> 5.9).
+//
 // The running O is kept in units of 2^40: a sum of 2^24 weights of up to 2^15
 // times values at the end of bf16's range stays finite, and at V scales of
 // 2^-100, the smallest, fp32's subnormals still hold 16 bits of a block's
-// largest.  int8 products come 2^24 of it too small already.
-template <int FMT>
-constexpr float kValueUnit = FMT == RV_KV8_INT8 ? 0x1p-16f : 0x1p-40f;
+// largest.
 constexpr float kOutUnit = 0x1p40f;
 // No factor of a score passes fp32's range before the score does.  Query rows
 // stand at 2^15 (int8: the top of fp16's range) or 2^4 instead of 2^0, which
@@ -171,16 +176,16 @@ __device__ __forceinline__ I8Const i8_const() {
   asm volatile("mov.b32 %0, 0x00ff00ff; mov.b32 %1, 0x00800080;" : "=r"(c.mask), "=r"(c.flip));
   return c;
 }
-__device__ __forceinline__ uint32_t and_xor(uint32_t x, I8Const c) {
+__device__ __forceinline__ uint32_t and_xor(uint32_t x, uint32_t mask, uint32_t flip) {
   uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(c.mask), "r"(c.flip));
+  asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(y) : "r"(x), "r"(mask), "r"(flip));
   return y;
 }
 template <int FMT>
 __device__ __forceinline__ void unpack_k(uint32_t w, uint32_t &lo, uint32_t &hi, I8Const c) {
   if (FMT == RV_KV8_INT8) {
-    lo = and_xor(w, c);
-    hi = and_xor(w >> 8, c);
+    lo = and_xor(w, c.mask, c.flip);
+    hi = and_xor(w >> 8, c.mask, c.flip);
   } else {
     asm("{.reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; cvt.rn.f16x2.e4m3x2 %1, h;}" : "=r"(lo), "=r"(hi) : "r"(w));
   }
@@ -189,10 +194,13 @@ __device__ __forceinline__ void unpack_k(uint32_t w, uint32_t &lo, uint32_t &hi,
 template <int FMT>
 __device__ __forceinline__ void unpack_v(uint32_t w0, uint32_t w1, uint32_t (&x)[4], I8Const c) {
   if (FMT == RV_KV8_INT8) {
-    x[0] = and_xor(prmt(w0, w1, 0x5410), c);
-    x[1] = and_xor(prmt(w0, w1, 0x6521), c);
-    x[2] = and_xor(prmt(w0, w1, 0x7632), c);
-    x[3] = and_xor(prmt(w0, w1, 0x4703), c);
+    constexpr uint32_t k1152 = 0x64806480u;  // the pair of fp16 1152; also the exponent of 1024 and the flip of a byte's sign
+    x[0] = prmt(w0, w1, 0x5410);
+    x[1] = prmt(w0, w1, 0x6521);
+    x[2] = prmt(w0, w1, 0x7632);
+    x[3] = prmt(w0, w1, 0x4703);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = h2_bits(__hsub2(bits_h2(and_xor(x[i], c.mask, k1152)), bits_h2(k1152)));
   } else {
     const uint32_t a = prmt(w0, w1, 0x5140), b = prmt(w0, w1, 0x7362);
     unpack_k<FMT>(a, x[0], x[1], c);
@@ -787,7 +795,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
       for (int i = 0; i < NG; ++i)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const float x = fs[TM + i * GS] * kValueUnit<FMT>;
+          const float x = fs[TM + i * GS] * (1.f / kOutUnit);
           vs[i][nt] = f2(x, x);
         }
 #pragma unroll 1
@@ -800,31 +808,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             const int2 sn = see(nt);
             vs[i][nt] = f2(sn.x <= p0 + 16 * GS * i ? 0.f : x.x, sn.y <= p0 + 16 * GS * i ? 0.f : x.y);
           }
-      }
-      float bias[NG][NT][2];  // where the products' sums begin
-      if (FMT == RV_KV8_INT8) {
-        const uint32_t one[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
-#pragma unroll
-        for (int i = 0; i < NG; ++i) {
-          float x[NT][4];
-#pragma unroll
-          for (int j = 0; j < GS; ++j) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (j == 0) mma16_from(x[nt], one, pb[i * GS][nt][0], pb[i * GS][nt][1], 0.f, 0.f);
-              else mma16(x[nt], one, pb[i * GS + j][nt][0], pb[i * GS + j][nt][1]);
-            }
-            if (LO) {
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16(x[nt], one, pl[i * GS + j][nt][0], pl[i * GS + j][nt][1]);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            bias[i][nt][0] = -kBias * x[nt][0];
-            bias[i][nt][1] = -kBias * x[nt][1];
-          }
-        }
       }
       // ---- O^T += vs (V^T P^T)
       // (words of a V row that a thread takes: all at once, or where registers
@@ -867,7 +850,6 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
             f[i][1][2 * hb] = x[2];
             f[i][1][2 * hb + 1] = x[3];
           }
-        constexpr bool I8 = FMT == RV_KV8_INT8;
         constexpr int HH = NT == 1 ? 2 : 1;  // tiles whose sums run side by side
 #pragma unroll
         for (int h0 = 0; h0 < 2; h0 += HH)
@@ -881,7 +863,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
               for (int h = 0; h < HH; ++h)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  if (j == 0) mma16_from(acc[h][nt], f[st][h0 + h], pb[st][nt][0], pb[st][nt][1], I8 ? bias[i][nt][0] : 0.f, I8 ? bias[i][nt][1] : 0.f);
+                  if (j == 0) mma16_from(acc[h][nt], f[st][h0 + h], pb[st][nt][0], pb[st][nt][1], 0.f, 0.f);
                   else mma16(acc[h][nt], f[st][h0 + h], pb[st][nt][0], pb[st][nt][1]);
                 }
               if (LO) {
