@@ -468,6 +468,77 @@ int rv_kv8_attention(const rv_kv8 *cache, const rv_heads *q, const rv_heads *out
  * arguments are bad.  Enough for every smaller B and T. */
 size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads);
 
+/* Several answers to one prompt: rows that begin with the same positions.
+ *
+ * Copy rows of a cache to rows of the same or another one: pair i makes row
+ * d_to[i] of dst hold the first d_len[i] positions of row d_from[i] of src
+ * (d_len NULL: as many as both caches have room for), so that it may be read
+ * or continued there as the source could be: at d_len[i] if the source could go
+ * back to that position (rv_kv8_append).  A prompt is forked to the rows that go
+ * on from it, beams are put into a new order, finished rows are closed up.  All
+ * pairs are copied at once, as if every source were read before any
+ * destination is written: rows may change places in one call, and a source may
+ * be named by any number of pairs.  Of several pairs with one destination the
+ * last counts.  Codes, their blocks' scales (the open block's whole) and the
+ * row's tail are copied; what the destination holds behind them stays.  Pairs
+ * with a negative row are passed over; rows at or beyond the cache's max_batch
+ * are too, and lengths outside 0 .. the smaller max_seq are taken as the
+ * nearer end: a row or a length that is too large sets bit 6 (64) of *d_err (or
+ * NULL: not reported).  src and dst agree in n_kv_heads, head_dim, block,
+ * format and act_dtype; they are one cache (all six pointers and max_seq the
+ * same) or have no memory in common.  n is at most 1024. */
+int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const int32_t *d_from, const int32_t *d_to, const int32_t *d_len,
+                int32_t *d_err, void *stream);
+
+/* Attention of T new tokens per row over a prefix that rows share and over each
+ * row's own cache: `fan` consecutive rows go with one row of `prefix` (row b
+ * with row b / fan), whose K and V are read once for all of them.  Query token t
+ * of row b sees the first d_prefix_len[b / fan] positions of the prefix row
+ * (NULL: max_seq of them; values outside 0..max_seq are taken as the nearer end)
+ * and positions 0 .. d_pos[b] + t of row b of `cache`, at most max_seq of them
+ * (none where d_pos[b] + t < 0); what it sees nothing of gives zeros.  Own
+ * positions count from the prefix's end: rotary positions are d_prefix_len + own
+ * position.  prefix and cache agree in n_kv_heads, head_dim and act_dtype; their
+ * formats, blocks and lengths may differ.  q, out, scale, d_count, d_lse and
+ * precision are as in rv_kv8_attention; the product of a weight and its block's
+ * V scale is rounded to fp16 (fp16 caches and RV_F32 outputs: two fp16 terms)
+ * and held down to 2^-31 of the largest weight times the largest V scale of the
+ * prefix.  Every wait inside is bounded: one that runs out sets bit 4 (16) of
+ * *d_err (or NULL: not reported), and the outputs are then not to be used.
+ * workspace: rv_kv8_attention_shared_workspace bytes, 16-byte aligned, no
+ * contents needed or kept; calls that may run at the same time need one each. */
+int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, int fan,
+                            float scale, const int32_t *d_prefix_len, const int32_t *d_pos, const int32_t *d_count, float *d_lse,
+                            int32_t *d_err, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of rv_kv8_attention_shared for up to B rows, T tokens and
+ * n_heads query heads on the current device; 0 with rv_last_error() set if the
+ * arguments are bad.  Enough for every smaller B and T with the same fan. */
+size_t rv_kv8_attention_shared_workspace(const rv_kv8 *prefix, const rv_kv8 *cache, int B, int T, int fan, int n_heads);
+
+/* Draw each row's next token from its logits.  d_logits [B] rows of `vocab`
+ * numbers of `dtype`, `stride` elements apart (any alignment that dtype has).
+ * NaN and -infinity are absent: they are never drawn.  Per row (NULL: off):
+ *   d_temperature  1 where NULL; 0, negative or NaN: the largest logit, the
+ *                  lowest index of equal ones (d_u is not used)
+ *   d_top_k        keep the first k in order of descending logits, equal ones
+ *                  by index; 0 or negative: all
+ *   d_top_p        of those, keep the ones before which less than top_p of
+ *                  their weight lies in that order (the first at least); 1,
+ *                  above or NaN: all
+ *   d_min_p        keep those of at least min_p of the largest weight (1 at
+ *                  most); 0, negative or NaN: all
+ * The weight of logit x is w = round(2^40 exp((x - max) / temperature)), a whole
+ * number: whatever weighs less than 2^-41 of the largest is never drawn, and the
+ * result does not depend on the order of any sum.  d_ids[b] is the first token,
+ * by index, up to which more than d_u[b] of the kept weight lies (d_u in [0, 1);
+ * below or NaN: 0, above: just below 1), d_logprob[b] (or NULL) the natural log
+ * of its part of the kept weight.  A row without any token gives -1 and
+ * -infinity.  1 <= vocab <= 262144, B <= 65535.  Weights are computed to 2^-29 of
+ * themselves; sums, cuts and the draw are exact on them. */
+int rv_sample(const void *d_logits, int dtype, int64_t stride, int B, int vocab, const float *d_temperature, const int32_t *d_top_k,
+              const float *d_top_p, const float *d_min_p, const float *d_u, int32_t *d_ids, float *d_logprob, void *stream);
+
 /* Rotary frequencies of a loaded model for contexts longer than its own
  * (rv_rope_config above): cfg's head_dim must be the model's, rotary_dim the
  * whole head and the layout RV_ROPE_HALF (RV_EINVAL otherwise).  NULL: back to

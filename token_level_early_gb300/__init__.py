@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_HERE, "librv.so")
 _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_ROOT, "_build")
 SOURCES = ["api.cu", "decode_b1.cu", "attention.cu", "general.cu", "quant.cu", "noalloc.cu", "stream.cu", "gemm_tc.cu", "rows_mma.cu",
-           "rope.cu", "kv8.cu", "kv8_attention.cu", "kv8_attention_e4m3.cu"]
+           "rope.cu", "kv8.cu", "kv8_attention.cu", "kv8_attention_e4m3.cu",
+           "kv8_copy.cu", "kv8_shared.cu", "sample.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 RV_OK, RV_EINVAL, RV_ENOMEM, RV_ECUDA, RV_ECAPACITY, RV_ESTATE, RV_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6
@@ -32,7 +33,8 @@ EXPORTED = ("rv_last_error", "rv_load_model", "rv_quantize_river", "rv_export_ri
             "rv_debug_dump", "rv_kv_bytes", "rv_param_bytes", "rv_free_model", "rv_time_kernel", "rv_greedy_head_noalloc", "rv_offload_backbone",
             "rv_set_option", "rv_debug_fail_alloc", "rv_decode_attention_plan",
             "rv_rope_init", "rv_rope", "rv_kv8_append", "rv_kv8_read", "rv_kv8_attention", "rv_kv8_attention_workspace",
-            "rv_set_rope", "rv_kv_cache_bytes")
+            "rv_set_rope", "rv_kv_cache_bytes",
+            "rv_kv8_copy", "rv_kv8_attention_shared", "rv_kv8_attention_shared_workspace", "rv_sample")
 OPT_DECODE_ENGINE, ENGINE_CHAIN, ENGINE_PERSISTENT = 0, 0, 1
 OPT_QUANTIZER, QUANT_RTN, QUANT_HQQ = 1, 0, 1
 OPT_WAIT_LIMIT_US = 2
@@ -172,6 +174,10 @@ def lib():
         "rv_kv8_read": ([kp, hp, hp, i32, i32, vp, vp, vp, vp], i32),
         "rv_kv8_attention": ([kp, hp, hp, i32, i32, f32, vp, vp, vp, vp, sz, vp], i32),
         "rv_kv8_attention_workspace": ([kp, i32, i32, i32], sz),
+        "rv_kv8_copy": ([kp, kp, i32, vp, vp, vp, vp, vp], i32),
+        "rv_kv8_attention_shared": ([kp, kp, hp, hp, i32, i32, i32, f32, vp, vp, vp, vp, vp, vp, sz, vp], i32),
+        "rv_kv8_attention_shared_workspace": ([kp, kp, i32, i32, i32, i32], sz),
+        "rv_sample": ([vp, i32, ctypes.c_int64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp], i32),
         "rv_set_rope": ([vp, ctypes.POINTER(RopeConfig)], i32),
         "rv_kv_cache_bytes": ([vp], sz),
     })
@@ -274,6 +280,36 @@ def kv8_attention(cache: KV8, q: Heads, out: Heads, B: int, T: int, scale: float
     """rv_kv8_attention: attention of T new tokens per row over the cache."""
     _check(lib().rv_kv8_attention(cache, q, out, B, T, scale, d_pos, d_count, d_lse, workspace, workspace_bytes,
                                   stream))
+
+
+def kv8_copy(src: KV8, dst: KV8, n: int, d_from: int, d_to: int, d_len: Optional[int] = None, d_err: Optional[int] = None,
+             stream: Optional[int] = None):
+    """rv_kv8_copy: row d_to[i] of dst becomes row d_from[i] of src, all n pairs at once."""
+    _check(lib().rv_kv8_copy(src, dst, n, d_from, d_to, d_len, d_err, stream))
+
+
+def kv8_attention_shared_workspace(prefix: KV8, cache: KV8, B: int, T: int, fan: int, n_heads: int) -> int:
+    """rv_kv8_attention_shared_workspace: bytes of workspace for kv8_attention_shared."""
+    n = lib().rv_kv8_attention_shared_workspace(prefix, cache, B, T, fan, n_heads)
+    if n == 0 and lib().rv_last_error():
+        raise RVError(RV_EINVAL, lib().rv_last_error().decode(errors="replace"))
+    return int(n)
+
+
+def kv8_attention_shared(prefix: KV8, cache: KV8, q: Heads, out: Heads, B: int, T: int, fan: int, scale: float,
+                         d_prefix_len: Optional[int], d_pos: Optional[int], d_count: Optional[int], d_lse: Optional[int],
+                         d_err: Optional[int], workspace: Optional[int], workspace_bytes: int, stream: Optional[int] = None):
+    """rv_kv8_attention_shared: attention over a prefix that `fan` rows share and over each row's own cache."""
+    _check(lib().rv_kv8_attention_shared(prefix, cache, q, out, B, T, fan, scale, d_prefix_len, d_pos, d_count, d_lse, d_err,
+                                         workspace, workspace_bytes, stream))
+
+
+def sample(d_logits: int, dtype: int, stride: int, B: int, vocab: int, d_temperature: Optional[int], d_top_k: Optional[int],
+           d_top_p: Optional[int], d_min_p: Optional[int], d_u: int, d_ids: int, d_logprob: Optional[int] = None,
+           stream: Optional[int] = None):
+    """rv_sample: draw each row's next token with temperature, top-k, top-p and min-p from the numbers d_u."""
+    _check(lib().rv_sample(d_logits, dtype, stride, B, vocab, d_temperature, d_top_k, d_top_p, d_min_p, d_u, d_ids, d_logprob,
+                           stream))
 
 
 def config_of(shape, max_batch: int, max_seq: int) -> RVConfig:

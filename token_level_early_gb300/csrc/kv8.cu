@@ -320,7 +320,7 @@ cudaError_t launch_kv8_read(const Kv8 &c, const Kv8Io &io, int out_dtype, cudaSt
 
 using namespace rv;
 
-namespace {
+namespace rv {
 
 int check_cache(const rv_kv8 *c, bool pointers) {
   if (!c) return op_fail(RV_EINVAL, "null pointer");
@@ -387,7 +387,7 @@ int sm_count(int *n) {
   return launched("device query", e);
 }
 
-}  // namespace
+}  // namespace rv
 
 extern "C" int rv_kv8_append(const rv_kv8 *cache, const rv_heads *k, const rv_heads *v, int B, int T,
                              const int32_t *d_pos, const int32_t *d_count, int32_t *d_err, void *stream) {

@@ -303,6 +303,11 @@ __device__ __forceinline__ float4 ld_cluster4(unsigned at, int k) {
 // 4 elements of an output row from its joined state (x = weighted sum in units
 // of kOutUnit, mm = reference in base 2, ll = sum).
 __device__ __forceinline__ void write_out(const Kv8AttnArgs &a, int b, int t, int h, int d, float4 x, float mm, float ll) {
+  if (a.raw) {
+    *reinterpret_cast<float4 *>(static_cast<float *>(a.out.p) + b * a.out.sb + t * a.out.st + h * a.out.sh + d) = x;
+    if (d == 0) a.raw[((int64_t)b * a.T + t) * a.H + h] = make_float2(mm, ll);
+    return;
+  }
   const float f = ll == 0.f ? 0.f : kOutUnit / ll;  // nothing seen: zeros
   x.x *= f; x.y *= f; x.z *= f; x.w *= f;
   const int act = a.c.act;

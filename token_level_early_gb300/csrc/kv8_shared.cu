@@ -1,0 +1,372 @@
+// Attention of new tokens over a prefix that several rows share and over each
+// row's own positions.
+//
+// out = (sum over the prefix + sum over the own positions) of w v / sum of w:
+// three kernels leave states (reference m, sum l, weighted sum O) and join them.
+// The own positions are the cache attention's (kv8_attention.cuh), which here
+// leaves its rows' states.  For the prefix, the fan x T x (H / Hkv) query rows
+// that share a KV head of a prefix row are taken together.
+#include "kv8_attention.cuh"
+#include "ops.cuh"
+
+namespace rv {
+namespace kv8s {
+
+using kv8a::ex2;
+using kv8a::kLog2e;
+using kv8a::kOutUnit;
+
+constexpr int kTile = 128;   // positions of a tile
+constexpr int kRows = 256;   // query rows of a unit at most
+
+// A unit is one prefix row, KV head and group of up to kRows query rows; its
+// tiles lie in one line with all others, which is cut evenly over the blocks.
+// Block c that takes a part of unit u leaves its state in slot c + u (both rise
+// along the line, so no two parts share one).
+struct SharedArgs {
+  Kv8 c;  // the prefix
+  Heads q;
+  int q_f32;
+  int H, B, T, fan, P;
+  int rows, groups, slot_rows;  // query rows of a prefix row and KV head, units of them, rows of a slot
+  float scale;
+  const int32_t *plen, *count;
+  int32_t *err;
+  int64_t *line;  // [P + 2]: where each prefix row's units begin in the line, its end, the length of a piece
+  float *slots;   // [blocks + units][slot_rows][hd + 2]
+  int lo;         // weights as two fp16 terms
+};
+
+__host__ __device__ __forceinline__ size_t slot_floats(int slot_rows, int hd) { return (size_t)slot_rows * (hd + 2); }
+
+__device__ __forceinline__ int prefix_len(const SharedArgs &a, int p) {
+  const int n = a.plen ? a.plen[p] : a.c.T;
+  return min(max(n, 0), a.c.T);
+}
+__device__ __forceinline__ int prefix_tiles(const SharedArgs &a, int p) { return (prefix_len(a, p) + kTile - 1) / kTile; }
+
+// Query row i of prefix row p: token i / grp of its rows' tokens, head i % grp.
+struct QueryRow {
+  int b, t;
+  bool live;
+};
+__device__ __forceinline__ QueryRow query_row(const SharedArgs &a, int p, int i, int grp) {
+  QueryRow r;
+  const int k = i / grp, f = k / a.T;
+  r.b = p * a.fan + f;
+  r.t = k - f * a.T;
+  r.live = i < a.rows && r.b < a.B;
+  if (r.live) r.live = r.t < row_count(a.count, r.b, a.T);
+  return r;
+}
+
+// The line: this block's piece, and the prefix row that it begins in.  Every
+// block computes it; block 0 leaves it for the join.
+constexpr int kMinTiles = 2;  // of a piece
+struct Piece {
+  int64_t begin, end, off;  // off: into row p
+  int p;
+};
+template <int THREADS>
+__device__ Piece cut_line(const SharedArgs &a, int64_t *scratch /* THREADS + 2 */) {
+  const int tid = threadIdx.x, per = (a.P + THREADS - 1) / THREADS, p0 = min(a.P, tid * per), p1 = min(a.P, p0 + per);
+  int64_t mine = 0;
+  const int64_t units = (int64_t)a.c.Hkv * a.groups;
+  for (int p = p0; p < p1; ++p) mine += units * prefix_tiles(a, p);
+  scratch[tid] = mine;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int i = 0; i < THREADS; ++i) {
+    const int64_t x = scratch[i];
+    if (i < tid) before += x;
+    total += x;
+  }
+  const int64_t piece = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinTiles);
+  Piece w;
+  w.begin = piece * blockIdx.x;
+  w.end = min(total, w.begin + piece);
+  int64_t at = before;
+  for (int p = p0; p < p1; ++p) {
+    const int64_t n = units * prefix_tiles(a, p);
+    if (blockIdx.x == 0) a.line[p] = at;
+    if (w.begin >= at && w.begin < at + n) {
+      scratch[THREADS] = p;
+      scratch[THREADS + 1] = w.begin - at;
+    }
+    at += n;
+  }
+  if (blockIdx.x == 0 && tid == 0) {
+    a.line[a.P] = total;
+    a.line[a.P + 1] = piece;
+  }
+  __syncthreads();
+  w.p = (int)scratch[THREADS];
+  w.off = scratch[THREADS + 1];
+  return w;
+}
+
+// ------------------------------------------------------------------ the prefix
+
+// A warp per query row: lanes take positions for the scores and elements for
+// the weighted sum.
+template <int FMT, int HD>
+__global__ void __launch_bounds__(256) k_prefix(const __grid_constant__ SharedArgs a) {
+  __shared__ int64_t scratch[258];
+  __shared__ float s_q[8][HD];
+  pdl_wait();
+  Piece w = cut_line<256>(a, scratch);
+  const Kv8 &c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = a.H / c.Hkv, lb = __ffs(c.block) - 1;
+  int64_t at = w.begin, off = w.off;
+  int p = w.p;
+  while (at < w.end && p < a.P) {  // (p: only if the lengths changed under the kernel)
+    const int tiles = prefix_tiles(a, p);
+    const int64_t in_row = (int64_t)c.Hkv * a.groups * tiles;
+    if (off >= in_row) { off -= in_row; ++p; continue; }
+    const int unit = (int)(off / tiles), t0 = (int)(off - (int64_t)unit * tiles), take = (int)min((int64_t)(tiles - t0), w.end - at);
+    const int g = unit / a.groups, row0 = (unit - g * a.groups) * kRows, n = prefix_len(a, p);
+    const int64_t u = ((int64_t)p * c.Hkv + g) * a.groups + (unit - g * a.groups), kvrow = (int64_t)p * c.Hkv + g;
+    float *slot = a.slots + (blockIdx.x + u) * slot_floats(a.slot_rows, HD);
+    for (int i = warp; i < a.slot_rows; i += 8) {
+      const QueryRow r = query_row(a, p, row0 + i, grp);
+      if (!r.live) continue;
+      const int h = g * grp + (row0 + i) % grp;
+      const int64_t o = r.b * a.q.sb + r.t * a.q.st + h * a.q.sh;
+      __syncwarp();
+      for (int d = lane; d < HD; d += 32)
+        s_q[warp][d] = a.q_f32 ? round_act(static_cast<const float *>(a.q.p)[o + d], c.act) : act_to_f(static_cast<const uint16_t *>(a.q.p)[o + d], c.act);
+      __syncwarp();
+      float m = -INFINITY, l = 0.f, x[HD / 32];
+#pragma unroll
+      for (int d = 0; d < HD / 32; ++d) x[d] = 0.f;
+      for (int p0 = t0 * kTile; p0 < min(n, (t0 + take) * kTile); p0 += 32) {
+        const int pos = p0 + lane;
+        float s = -INFINITY, vs = 0.f;
+        if (pos < n) {
+          const uint8_t *k = c.codes[0] + (kvrow * c.N + pos) * HD;
+          float dot = 0.f;
+          for (int d = 0; d < HD; ++d) {
+            const uint8_t v = k[d];
+            dot = fmaf(FMT == RV_KV8_INT8 ? (float)(int8_t)v : __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3))), s_q[warp][d], dot);
+          }
+          s = dot * c.scale[0][kvrow * (c.N >> lb) + (pos >> lb)] * a.scale * kLog2e;
+          vs = c.scale[1][kvrow * (c.N >> lb) + (pos >> lb)] * (1.f / kOutUnit);
+        }
+        float top = warp_max(s);
+        if (s != s) top = s;
+        const float mm = fmaxf(m, top), base = mm == -INFINITY ? 0.f : mm, al = ex2(m - base), e = pos < n ? ex2(s - base) : 0.f;
+        l = l * al + warp_sum(e);
+        m = mm;
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) x[d] *= al;
+        for (int j = 0; j < 32 && p0 + j < n; ++j) {
+          const float f = __shfl_sync(0xffffffffu, e, j) * __shfl_sync(0xffffffffu, vs, j);
+          const uint8_t *v = c.codes[1] + (kvrow * c.N + p0 + j) * HD;
+#pragma unroll
+          for (int d = 0; d < HD / 32; ++d) {
+            const uint8_t y = v[d * 32 + lane];
+            x[d] = fmaf(FMT == RV_KV8_INT8 ? (float)(int8_t)y : __half2float(__half(__nv_cvt_fp8_to_halfraw(y, __NV_E4M3))), f, x[d]);
+          }
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < HD / 32; ++d) slot[(size_t)i * HD + d * 32 + lane] = x[d];
+      if (lane == 0) {
+        slot[(size_t)a.slot_rows * HD + 2 * i] = m;
+        slot[(size_t)a.slot_rows * HD + 2 * i + 1] = l;
+      }
+    }
+    at += take;
+    off += take;
+  }
+}
+
+// ------------------------------------------------------------------ join
+
+// A warp per output row: the prefix's parts and the own positions' state.
+constexpr int kJoin = 6;
+template <int HD>
+__global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ SharedArgs a, const __grid_constant__ Kv8AttnArgs f, const float *own,
+                                                     const float2 *raw) {
+  constexpr int PER = HD / 32;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (row >= (int64_t)a.B * a.T * a.H) return;
+  const int h = (int)(row % a.H), b = (int)(row / a.H / a.T), t = (int)(row / a.H - (int64_t)b * a.T);
+  if (t >= row_count(a.count, b, a.T)) return;
+  const int grp = a.H / a.c.Hkv, p = b / a.fan, g = h / grp, i = ((b - p * a.fan) * a.T + t) * grp + h - g * grp, group = i / kRows, rr = i - group * kRows;
+  const int tiles = prefix_tiles(a, p);
+  const float2 s0 = raw[row];
+  float mm = s0.y == 0.f ? -INFINITY : s0.x, ll = s0.y, x[PER];
+#pragma unroll
+  for (int d = 0; d < PER; ++d) x[d] = own[row * HD + lane * PER + d];
+  if (tiles) {
+    const int64_t piece = a.line[a.P + 1], begin = a.line[p] + ((int64_t)g * a.groups + group) * tiles;
+    const int c0 = (int)(begin / piece), c1 = (int)((begin + tiles - 1) / piece);
+    const int64_t u = ((int64_t)p * a.c.Hkv + g) * a.groups + group;
+    for (int c = c0; c <= c1; c += kJoin) {
+      float sm[kJoin], sl[kJoin], y[kJoin][PER], top = mm;
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        sm[j] = -INFINITY;
+        sl[j] = 0.f;
+#pragma unroll
+        for (int d = 0; d < PER; ++d) y[j][d] = 0.f;
+        if (c + j <= c1) {
+          const float *s = a.slots + (c + j + u) * slot_floats(a.slot_rows, HD);
+          const float2 v = *reinterpret_cast<const float2 *>(s + (size_t)a.slot_rows * HD + 2 * rr);
+          sm[j] = v.x;
+          sl[j] = v.y;
+#pragma unroll
+          for (int d = 0; d < PER; ++d) y[j][d] = s[(size_t)rr * HD + lane * PER + d];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) top = fmaxf(top, sm[j]);
+      const float base = top == -INFINITY ? 0.f : top, old = ex2(mm - base);
+      ll *= old;
+#pragma unroll
+      for (int d = 0; d < PER; ++d) x[d] *= old;
+#pragma unroll
+      for (int j = 0; j < kJoin; ++j) {
+        const float e = ex2(sm[j] - base);
+        ll = fmaf(sl[j], e, ll);
+#pragma unroll
+        for (int d = 0; d < PER; ++d) x[d] = fmaf(y[j][d], e, x[d]);
+      }
+      mm = top;
+    }
+  }
+  float4 v;
+  if (PER == 4) v = make_float4(x[0], x[1], x[PER - 2], x[PER - 1]);
+  else v = make_float4(x[0], x[1], __shfl_down_sync(0xffffffffu, x[0], 1), __shfl_down_sync(0xffffffffu, x[1], 1));
+  if (PER == 4 || !(lane & 1)) kv8a::write_out(f, b, t, h, lane * PER, v, mm, ll);
+}
+
+struct Plan {
+  int P, rows, groups, slot_rows;
+  int64_t units;
+  size_t own_work, own_out, raw, line, slots, bytes;  // offsets
+};
+Plan plan_of(const Kv8 &cache, int B, int T, int fan, int H, int n_sm) {
+  Plan s;
+  if (fan > B) fan = B;
+  s.P = (B + fan - 1) / fan;
+  s.rows = fan * T * (H / cache.Hkv);
+  s.groups = (s.rows + kRows - 1) / kRows;
+  s.slot_rows = s.rows < kRows ? s.rows : kRows;
+  s.units = (int64_t)s.P * cache.Hkv * s.groups;
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  size_t at = 0;
+  s.own_work = at; at += up(kv8_attention_work(cache, B, T, H, n_sm));
+  s.own_out = at; at += up((size_t)B * T * H * cache.hd * 4);
+  s.raw = at; at += up((size_t)B * T * H * 8);
+  s.line = at; at += up((size_t)(s.P + 2) * 8);
+  s.slots = at; at += up((size_t)(n_sm + s.units) * slot_floats(s.slot_rows, cache.hd) * 4);
+  s.bytes = at;
+  return s;
+}
+
+template <int FMT, int HD>
+cudaError_t launch_prefix(const SharedArgs &a, int n_sm, cudaStream_t s) {
+  return launch_k(k_prefix<FMT, HD>, dim3(n_sm), dim3(256), 0, s, 1, a);
+}
+
+int check_shared(const rv_kv8 *prefix, const rv_kv8 *cache, int B, int T, int fan, int heads, bool pointers) {
+  if (int rc = check_cache(prefix, pointers)) return rc;
+  if (int rc = check_cache(cache, pointers)) return rc;
+  if (prefix->n_kv_heads != cache->n_kv_heads || prefix->head_dim != cache->head_dim || prefix->act_dtype != cache->act_dtype)
+    return op_fail(RV_EINVAL, "prefix and cache differ in n_kv_heads, head_dim or act_dtype");
+  if (int rc = check_rows(cache, B, T)) return rc;
+  if (T > 16) return op_fail(RV_EINVAL, "T must be in 1..16");
+  if (fan < 1) return op_fail(RV_EINVAL, "fan must be at least 1");
+  if ((B + (int64_t)fan - 1) / fan > prefix->max_batch) return op_fail(RV_EINVAL, "B / fan above the prefix's max_batch");
+  if (heads < 1 || heads > 65535 || heads % cache->n_kv_heads) return op_fail(RV_EINVAL, "query heads must be a multiple of n_kv_heads");
+  if ((int64_t)B * T * heads > INT32_MAX / 8) return op_fail(RV_EINVAL, "B x T x heads above 2^28");
+  return RV_OK;
+}
+
+}  // namespace kv8s
+}  // namespace rv
+
+// ==================================================================== C ABI
+
+using namespace rv;
+
+extern "C" size_t rv_kv8_attention_shared_workspace(const rv_kv8 *prefix, const rv_kv8 *cache, int B, int T, int fan, int n_heads) {
+  set_error_message("");
+  int n_sm = 0;
+  if (kv8s::check_shared(prefix, cache, B, T, fan, n_heads, false) || sm_count(&n_sm)) return 0;
+  return kv8s::plan_of(kv8_of(cache), B, T, fan, n_heads, n_sm).bytes;
+}
+
+extern "C" int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, int fan,
+                                       float scale, const int32_t *d_prefix_len, const int32_t *d_pos, const int32_t *d_count, float *d_lse,
+                                       int32_t *d_err, void *workspace, size_t workspace_bytes, void *stream) {
+  set_error_message("");
+  if (int rc = check_cache(cache, true)) return rc;
+  if (int rc = check_heads("q", q, B > 0 ? B : 1, T > 0 ? T : 1, cache->head_dim, false)) return rc;
+  if (int rc = kv8s::check_shared(prefix, cache, B, T, fan, q->heads, true)) return rc;
+  if (int rc = check_heads("out", out, B, T, cache->head_dim, true)) return rc;
+  if (out->heads != q->heads) return op_fail(RV_EINVAL, "q and out differ in heads");
+  if (q->dtype != cache->act_dtype && q->dtype != RV_F32) return op_fail(RV_EINVAL, "q must be act_dtype or RV_F32");
+  if (out->dtype != cache->act_dtype && out->dtype != RV_F32) return op_fail(RV_EINVAL, "out must be act_dtype or RV_F32");
+  if (!(scale - scale == 0.f)) return op_fail(RV_EINVAL, "scale must be finite");
+  if (int rc = check_index(d_pos, d_count, reinterpret_cast<const int32_t *>(d_lse))) return rc;
+  if (int rc = check_index(d_prefix_len, nullptr, d_err)) return rc;
+  if (reinterpret_cast<uintptr_t>(workspace) & 15u) return op_fail(RV_EINVAL, "workspace not 16-byte aligned");
+  if (int rc = check_memory(cache, q->data, out->data, d_pos, d_count, d_lse)) return rc;
+  if (int rc = check_memory(prefix, nullptr, nullptr, d_prefix_len, nullptr, d_err)) return rc;
+  int n_sm = 0;
+  if (int rc = sm_count(&n_sm)) return rc;
+  const Kv8 c = kv8_of(cache);
+  const kv8s::Plan plan = kv8s::plan_of(c, B, T, fan, q->heads, n_sm);
+  if (workspace_bytes < plan.bytes) return op_fail(RV_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, plan.bytes);
+  if (!workspace) return op_fail(RV_EINVAL, "workspace: null pointer");
+  if (int rc = check_device("workspace", workspace)) return rc;
+  char *work = static_cast<char *>(workspace);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // the own positions
+  Kv8AttnArgs own{};
+  own.c = c;
+  own.q = heads_of(q);
+  own.out = Heads{work + plan.own_out, (int64_t)T * q->heads * c.hd, (int64_t)q->heads * c.hd, c.hd};
+  own.H = q->heads; own.B = B; own.T = T;
+  own.q_f32 = q->dtype == RV_F32;
+  own.out_dtype = RV_F32;
+  own.round_out = out->dtype != RV_F32;
+  own.scale = scale;
+  own.pos = d_pos; own.count = d_count;
+  own.raw = reinterpret_cast<float2 *>(work + plan.raw);
+  own.work = work + plan.own_work;
+  own.cluster = kv8_attention_cluster(c, B, T, own.H, n_sm, c.T);
+  if (int rc = launched("rv_kv8_attention_shared", launch_kv8_attention(own, n_sm, s, 1))) return rc;
+  // the prefix
+  kv8s::SharedArgs a{};
+  a.c = kv8_of(prefix);
+  a.q = heads_of(q);
+  a.q_f32 = own.q_f32;
+  a.H = own.H; a.B = B; a.T = T; a.fan = fan < B ? fan : B; a.P = plan.P;
+  a.rows = plan.rows; a.groups = plan.groups; a.slot_rows = plan.slot_rows;
+  a.scale = scale;
+  a.plen = d_prefix_len; a.count = d_count; a.err = d_err;
+  a.line = reinterpret_cast<int64_t *>(work + plan.line);
+  a.slots = reinterpret_cast<float *>(work + plan.slots);
+  a.lo = c.act == RV_F16 || out->dtype == RV_F32;
+  cudaError_t e = a.c.fmt == RV_KV8_INT8 ? (c.hd == 64 ? kv8s::launch_prefix<RV_KV8_INT8, 64>(a, n_sm, s) : kv8s::launch_prefix<RV_KV8_INT8, 128>(a, n_sm, s))
+                                         : (c.hd == 64 ? kv8s::launch_prefix<RV_KV8_E4M3, 64>(a, n_sm, s) : kv8s::launch_prefix<RV_KV8_E4M3, 128>(a, n_sm, s));
+  if (int rc = launched("rv_kv8_attention_shared", e)) return rc;
+  // the join
+  Kv8AttnArgs f = own;
+  f.out = heads_of(out);
+  f.out_dtype = out->dtype;
+  f.round_out = 0;
+  f.raw = nullptr;
+  f.lse = d_lse;
+  const dim3 grid((unsigned)(((int64_t)B * T * own.H + 7) / 8));
+  const float *own_out = static_cast<const float *>(own.out.p);
+  return launched("rv_kv8_attention_shared", launch_k(c.hd == 64 ? kv8s::k_shared_join<64> : kv8s::k_shared_join<128>, grid, dim3(256), 0, s, 1, a, f,
+                                                      own_out, (const float2 *)own.raw));
+}

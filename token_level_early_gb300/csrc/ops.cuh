@@ -91,6 +91,16 @@ int check_heads(const char *what, const rv_heads *h, int B, int T, int head_dim,
 int check_batch(int B, int T);
 // RV_EINVAL if p is not device (or managed) memory of the current device.
 int check_device(const char *what, const void *p);
+// A cache's descriptor; with `pointers`, that its memory is there and aligned.
+int check_cache(const rv_kv8 *c, bool pointers);
+// B rows of T tokens of a cache.
+int check_rows(const rv_kv8 *c, int B, int T);
+int check_index(const int32_t *pos, const int32_t *count, const int32_t *err);
+// Where every pointer of a call lives (after the checks that need no GPU).
+int check_memory(const rv_kv8 *c, const void *x, const void *y, const int32_t *pos, const int32_t *count, const void *more);
+// A launch's result as a status, with the message set.
+int launched(const char *what, cudaError_t e);
+int sm_count(int *n);
 
 // Rotary positions.
 struct RopeArgs {
@@ -130,6 +140,7 @@ struct Kv8AttnArgs {
   float scale;
   const int32_t *pos, *count;
   float *lse;
+  float2 *raw;  // not NULL: out (RV_F32) receives weighted sums as they are, raw [B][T][H] their reference and sum, for a join
   void *work;
   int cluster;  // blocks of a cluster (short contexts: a cluster per unit), or 0 (the cut line)
 };
