@@ -22,7 +22,7 @@ _CSRC = os.path.join(_HERE, "csrc")
 _BUILD = os.path.join(_ROOT, "_build")
 SOURCES = ["api.cu", "decode_b1.cu", "attention.cu", "general.cu", "quant.cu", "noalloc.cu", "stream.cu", "gemm_tc.cu", "rows_mma.cu",
            "rope.cu", "kv8.cu", "kv8_attention.cu", "kv8_attention_e4m3.cu",
-           "kv8_copy.cu", "kv8_shared.cu", "sample.cu"]
+           "kv8_copy.cu", "kv8_shared.cu", "kv8_shared_e4m3.cu", "sample.cu"]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 RV_OK, RV_EINVAL, RV_ENOMEM, RV_ECUDA, RV_ECAPACITY, RV_ESTATE, RV_ETIMEOUT = 0, -1, -2, -3, -4, -5, -6

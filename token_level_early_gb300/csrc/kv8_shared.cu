@@ -6,180 +6,10 @@
 // The own positions are the cache attention's (kv8_attention.cuh), which here
 // leaves its rows' states.  For the prefix, the fan x T x (H / Hkv) query rows
 // that share a KV head of a prefix row are taken together.
-#include "kv8_attention.cuh"
-#include "ops.cuh"
+#include "kv8_shared.cuh"
 
 namespace rv {
 namespace kv8s {
-
-using kv8a::ex2;
-using kv8a::kLog2e;
-using kv8a::kOutUnit;
-
-constexpr int kTile = 128;   // positions of a tile
-constexpr int kRows = 256;   // query rows of a unit at most
-
-// A unit is one prefix row, KV head and group of up to kRows query rows; its
-// tiles lie in one line with all others, which is cut evenly over the blocks.
-// Block c that takes a part of unit u leaves its state in slot c + u (both rise
-// along the line, so no two parts share one).
-struct SharedArgs {
-  Kv8 c;  // the prefix
-  Heads q;
-  int q_f32;
-  int H, B, T, fan, P;
-  int rows, groups, slot_rows;  // query rows of a prefix row and KV head, units of them, rows of a slot
-  float scale;
-  const int32_t *plen, *count;
-  int32_t *err;
-  int64_t *line;  // [P + 2]: where each prefix row's units begin in the line, its end, the length of a piece
-  float *slots;   // [blocks + units][slot_rows][hd + 2]
-  int lo;         // weights as two fp16 terms
-};
-
-__host__ __device__ __forceinline__ size_t slot_floats(int slot_rows, int hd) { return (size_t)slot_rows * (hd + 2); }
-
-__device__ __forceinline__ int prefix_len(const SharedArgs &a, int p) {
-  const int n = a.plen ? a.plen[p] : a.c.T;
-  return min(max(n, 0), a.c.T);
-}
-__device__ __forceinline__ int prefix_tiles(const SharedArgs &a, int p) { return (prefix_len(a, p) + kTile - 1) / kTile; }
-
-// Query row i of prefix row p: token i / grp of its rows' tokens, head i % grp.
-struct QueryRow {
-  int b, t;
-  bool live;
-};
-__device__ __forceinline__ QueryRow query_row(const SharedArgs &a, int p, int i, int grp) {
-  QueryRow r;
-  const int k = i / grp, f = k / a.T;
-  r.b = p * a.fan + f;
-  r.t = k - f * a.T;
-  r.live = i < a.rows && r.b < a.B;
-  if (r.live) r.live = r.t < row_count(a.count, r.b, a.T);
-  return r;
-}
-
-// The line: this block's piece, and the prefix row that it begins in.  Every
-// block computes it; block 0 leaves it for the join.
-constexpr int kMinTiles = 2;  // of a piece
-struct Piece {
-  int64_t begin, end, off;  // off: into row p
-  int p;
-};
-template <int THREADS>
-__device__ Piece cut_line(const SharedArgs &a, int64_t *scratch /* THREADS + 2 */) {
-  const int tid = threadIdx.x, per = (a.P + THREADS - 1) / THREADS, p0 = min(a.P, tid * per), p1 = min(a.P, p0 + per);
-  int64_t mine = 0;
-  const int64_t units = (int64_t)a.c.Hkv * a.groups;
-  for (int p = p0; p < p1; ++p) mine += units * prefix_tiles(a, p);
-  scratch[tid] = mine;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int i = 0; i < THREADS; ++i) {
-    const int64_t x = scratch[i];
-    if (i < tid) before += x;
-    total += x;
-  }
-  const int64_t piece = max((total + gridDim.x - 1) / gridDim.x, (int64_t)kMinTiles);
-  Piece w;
-  w.begin = piece * blockIdx.x;
-  w.end = min(total, w.begin + piece);
-  int64_t at = before;
-  for (int p = p0; p < p1; ++p) {
-    const int64_t n = units * prefix_tiles(a, p);
-    if (blockIdx.x == 0) a.line[p] = at;
-    if (w.begin >= at && w.begin < at + n) {
-      scratch[THREADS] = p;
-      scratch[THREADS + 1] = w.begin - at;
-    }
-    at += n;
-  }
-  if (blockIdx.x == 0 && tid == 0) {
-    a.line[a.P] = total;
-    a.line[a.P + 1] = piece;
-  }
-  __syncthreads();
-  w.p = (int)scratch[THREADS];
-  w.off = scratch[THREADS + 1];
-  return w;
-}
-
-// ------------------------------------------------------------------ the prefix
-
-// A warp per query row: lanes take positions for the scores and elements for
-// the weighted sum.
-template <int FMT, int HD>
-__global__ void __launch_bounds__(256) k_prefix(const __grid_constant__ SharedArgs a) {
-  __shared__ int64_t scratch[258];
-  __shared__ float s_q[8][HD];
-  pdl_wait();
-  Piece w = cut_line<256>(a, scratch);
-  const Kv8 &c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, grp = a.H / c.Hkv, lb = __ffs(c.block) - 1;
-  int64_t at = w.begin, off = w.off;
-  int p = w.p;
-  while (at < w.end && p < a.P) {  // (p: only if the lengths changed under the kernel)
-    const int tiles = prefix_tiles(a, p);
-    const int64_t in_row = (int64_t)c.Hkv * a.groups * tiles;
-    if (off >= in_row) { off -= in_row; ++p; continue; }
-    const int unit = (int)(off / tiles), t0 = (int)(off - (int64_t)unit * tiles), take = (int)min((int64_t)(tiles - t0), w.end - at);
-    const int g = unit / a.groups, row0 = (unit - g * a.groups) * kRows, n = prefix_len(a, p);
-    const int64_t u = ((int64_t)p * c.Hkv + g) * a.groups + (unit - g * a.groups), kvrow = (int64_t)p * c.Hkv + g;
-    float *slot = a.slots + (blockIdx.x + u) * slot_floats(a.slot_rows, HD);
-    for (int i = warp; i < a.slot_rows; i += 8) {
-      const QueryRow r = query_row(a, p, row0 + i, grp);
-      if (!r.live) continue;
-      const int h = g * grp + (row0 + i) % grp;
-      const int64_t o = r.b * a.q.sb + r.t * a.q.st + h * a.q.sh;
-      __syncwarp();
-      for (int d = lane; d < HD; d += 32)
-        s_q[warp][d] = a.q_f32 ? round_act(static_cast<const float *>(a.q.p)[o + d], c.act) : act_to_f(static_cast<const uint16_t *>(a.q.p)[o + d], c.act);
-      __syncwarp();
-      float m = -INFINITY, l = 0.f, x[HD / 32];
-#pragma unroll
-      for (int d = 0; d < HD / 32; ++d) x[d] = 0.f;
-      for (int p0 = t0 * kTile; p0 < min(n, (t0 + take) * kTile); p0 += 32) {
-        const int pos = p0 + lane;
-        float s = -INFINITY, vs = 0.f;
-        if (pos < n) {
-          const uint8_t *k = c.codes[0] + (kvrow * c.N + pos) * HD;
-          float dot = 0.f;
-          for (int d = 0; d < HD; ++d) {
-            const uint8_t v = k[d];
-            dot = fmaf(FMT == RV_KV8_INT8 ? (float)(int8_t)v : __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3))), s_q[warp][d], dot);
-          }
-          s = dot * c.scale[0][kvrow * (c.N >> lb) + (pos >> lb)] * a.scale * kLog2e;
-          vs = c.scale[1][kvrow * (c.N >> lb) + (pos >> lb)] * (1.f / kOutUnit);
-        }
-        float top = warp_max(s);
-        if (s != s) top = s;
-        const float mm = fmaxf(m, top), base = mm == -INFINITY ? 0.f : mm, al = ex2(m - base), e = pos < n ? ex2(s - base) : 0.f;
-        l = l * al + warp_sum(e);
-        m = mm;
-#pragma unroll
-        for (int d = 0; d < HD / 32; ++d) x[d] *= al;
-        for (int j = 0; j < 32 && p0 + j < n; ++j) {
-          const float f = __shfl_sync(0xffffffffu, e, j) * __shfl_sync(0xffffffffu, vs, j);
-          const uint8_t *v = c.codes[1] + (kvrow * c.N + p0 + j) * HD;
-#pragma unroll
-          for (int d = 0; d < HD / 32; ++d) {
-            const uint8_t y = v[d * 32 + lane];
-            x[d] = fmaf(FMT == RV_KV8_INT8 ? (float)(int8_t)y : __half2float(__half(__nv_cvt_fp8_to_halfraw(y, __NV_E4M3))), f, x[d]);
-          }
-        }
-      }
-#pragma unroll
-      for (int d = 0; d < HD / 32; ++d) slot[(size_t)i * HD + d * 32 + lane] = x[d];
-      if (lane == 0) {
-        slot[(size_t)a.slot_rows * HD + 2 * i] = m;
-        slot[(size_t)a.slot_rows * HD + 2 * i + 1] = l;
-      }
-    }
-    at += take;
-    off += take;
-  }
-}
 
 // ------------------------------------------------------------------ join
 
@@ -265,14 +95,11 @@ Plan plan_of(const Kv8 &cache, int B, int T, int fan, int H, int n_sm) {
   s.raw = at; at += up((size_t)B * T * H * 8);
   s.line = at; at += up((size_t)(s.P + 2) * 8);
   s.slots = at; at += up((size_t)(n_sm + s.units) * slot_floats(s.slot_rows, cache.hd) * 4);
-  s.bytes = at;
+  s.bytes = at + 240;  // the parts begin on 256-byte boundaries of a 16-byte aligned workspace
   return s;
 }
 
-template <int FMT, int HD>
-cudaError_t launch_prefix(const SharedArgs &a, int n_sm, cudaStream_t s) {
-  return launch_k(k_prefix<FMT, HD>, dim3(n_sm), dim3(256), 0, s, 1, a);
-}
+cudaError_t launch_prefix_int8(const SharedArgs &a, int n_sm, cudaStream_t s) { return launch_prefix_fmt<RV_KV8_INT8>(a, n_sm, s); }
 
 int check_shared(const rv_kv8 *prefix, const rv_kv8 *cache, int B, int T, int fan, int heads, bool pointers) {
   if (int rc = check_cache(prefix, pointers)) return rc;
@@ -326,7 +153,7 @@ extern "C" int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache
   if (workspace_bytes < plan.bytes) return op_fail(RV_EINVAL, "workspace of %zu bytes, %zu needed", workspace_bytes, plan.bytes);
   if (!workspace) return op_fail(RV_EINVAL, "workspace: null pointer");
   if (int rc = check_device("workspace", workspace)) return rc;
-  char *work = static_cast<char *>(workspace);
+  char *work = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~(uintptr_t)255);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the own positions
   Kv8AttnArgs own{};
@@ -355,8 +182,7 @@ extern "C" int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache
   a.line = reinterpret_cast<int64_t *>(work + plan.line);
   a.slots = reinterpret_cast<float *>(work + plan.slots);
   a.lo = c.act == RV_F16 || out->dtype == RV_F32;
-  cudaError_t e = a.c.fmt == RV_KV8_INT8 ? (c.hd == 64 ? kv8s::launch_prefix<RV_KV8_INT8, 64>(a, n_sm, s) : kv8s::launch_prefix<RV_KV8_INT8, 128>(a, n_sm, s))
-                                         : (c.hd == 64 ? kv8s::launch_prefix<RV_KV8_E4M3, 64>(a, n_sm, s) : kv8s::launch_prefix<RV_KV8_E4M3, 128>(a, n_sm, s));
+  const cudaError_t e = a.c.fmt == RV_KV8_INT8 ? kv8s::launch_prefix_int8(a, n_sm, s) : kv8s::launch_prefix_e4m3(a, n_sm, s);
   if (int rc = launched("rv_kv8_attention_shared", e)) return rc;
   // the join
   Kv8AttnArgs f = own;
