@@ -13,66 +13,105 @@ namespace kv8s {
 
 // ------------------------------------------------------------------ join
 
-// A warp per output row: the prefix's parts and the own positions' state.
-constexpr int kJoin = 6;
-template <int HD>
+// WPR warps an output row: the prefix's parts, up to kJoin of them on their way
+// at once, and the own positions' state.  What this takes is the latency of its
+// dependent loads where rows are few, and reading the states where they are many.
+constexpr int kJoin = 5;
+template <int PER>
+__device__ __forceinline__ void load_part(float (&x)[PER], const float *from) {
+  if (PER == 4) {
+    const float4 v = *reinterpret_cast<const float4 *>(from);
+    x[0] = v.x; x[1] = v.y; x[PER - 2] = v.z; x[PER - 1] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2 *>(from);
+    x[0] = v.x; x[1] = v.y;
+  }
+}
+template <int HD, int WPR>
 __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ SharedArgs a, const __grid_constant__ Kv8AttnArgs f, const float *own,
                                                      const float2 *raw) {
   constexpr int PER = HD / 32;
+  __shared__ __align__(16) float s_x[8][HD];
+  __shared__ float s_m[8], s_l[8];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (int64_t)a.B * a.T * a.H) return;
-  const int h = (int)(row % a.H), b = (int)(row / a.H / a.T), t = (int)(row / a.H - (int64_t)b * a.T);
-  if (t >= row_count(a.count, b, a.T)) return;
-  const int grp = a.H / a.c.Hkv, p = b / a.fan, g = h / grp, i = ((b - p * a.fan) * a.T + t) * grp + h - g * grp, group = i / kRows, rr = i - group * kRows;
-  const int tiles = prefix_tiles(a, p);
-  const float2 s0 = raw[row];
-  float mm = s0.y == 0.f ? -INFINITY : s0.x, ll = s0.y, x[PER];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int row = blockIdx.x * (8 / WPR) + warp / WPR, bt = row / a.H, h = row - bt * a.H, b = bt / a.T, t = bt - b * a.T;
+  const bool live = row < a.B * a.T * a.H && t < row_count(a.count, b, a.T);
+  float mm = -INFINITY, ll = 0.f, x[PER];
 #pragma unroll
-  for (int d = 0; d < PER; ++d) x[d] = own[row * HD + lane * PER + d];
-  if (tiles) {
-    const int64_t piece = a.line[a.P + 1], begin = a.line[p] + ((int64_t)g * a.groups + group) * tiles;
-    const int c0 = (int)(begin / piece), c1 = (int)((begin + tiles - 1) / piece);
-    const int64_t u = ((int64_t)p * a.c.Hkv + g) * a.groups + group;
-    for (int c = c0; c <= c1; c += kJoin) {
-      float sm[kJoin], sl[kJoin], y[kJoin][PER], top = mm;
+  for (int d = 0; d < PER; ++d) x[d] = 0.f;
+  if (live) {
+    const int grp = a.H / a.c.Hkv, p = b / a.fan, g = h / grp, i = ((b - p * a.fan) * a.T + t) * grp + h - g * grp, group = i / kRows, rr = i - group * kRows;
+    const int tiles = prefix_tiles(a, p), piece = a.line[a.P], begin = a.line[p] + (g * a.groups + group) * tiles;
+    if (sub == 0) {
+      const float2 v = raw[row];
+      mm = v.y == 0.f ? -INFINITY : v.x;
+      ll = v.y;
+      load_part(x, own + (int64_t)row * HD + lane * PER);
+    }
+    const int c0 = begin / piece, c1 = tiles ? (begin + tiles - 1) / piece : -1;
+    const float *slots = a.slots + (size_t)((p * a.c.Hkv + g) * a.groups + group) * slot_floats(a.slot_rows, HD);
+    for (int c = c0 + sub; c <= c1; c += kJoin * WPR) {
+      float2 v[kJoin];
+      float y[kJoin][PER], top = mm;
 #pragma unroll
       for (int j = 0; j < kJoin; ++j) {
-        sm[j] = -INFINITY;
-        sl[j] = 0.f;
+        v[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int d = 0; d < PER; ++d) y[j][d] = 0.f;
-        if (c + j <= c1) {
-          const float *s = a.slots + (c + j + u) * slot_floats(a.slot_rows, HD);
-          const float2 v = *reinterpret_cast<const float2 *>(s + (size_t)a.slot_rows * HD + 2 * rr);
-          sm[j] = v.x;
-          sl[j] = v.y;
-#pragma unroll
-          for (int d = 0; d < PER; ++d) y[j][d] = s[(size_t)rr * HD + lane * PER + d];
+        if (c + j * WPR <= c1) {
+          const float *s = slots + (size_t)(c + j * WPR) * slot_floats(a.slot_rows, HD);
+          v[j] = *reinterpret_cast<const float2 *>(s + (size_t)a.slot_rows * HD + 2 * rr);
+          load_part(y[j], s + (size_t)rr * HD + lane * PER);
         }
       }
 #pragma unroll
-      for (int j = 0; j < kJoin; ++j) top = fmaxf(top, sm[j]);
+      for (int j = 0; j < kJoin; ++j) top = fmaxf(top, v[j].x);
       const float base = top == -INFINITY ? 0.f : top, old = ex2(mm - base);
       ll *= old;
 #pragma unroll
       for (int d = 0; d < PER; ++d) x[d] *= old;
 #pragma unroll
       for (int j = 0; j < kJoin; ++j) {
-        const float e = ex2(sm[j] - base);
-        ll = fmaf(sl[j], e, ll);
+        const float e = ex2(v[j].x - base);
+        ll = fmaf(v[j].y, e, ll);
 #pragma unroll
         for (int d = 0; d < PER; ++d) x[d] = fmaf(y[j][d], e, x[d]);
       }
       mm = top;
     }
   }
-  float4 v;
-  if (PER == 4) v = make_float4(x[0], x[1], x[PER - 2], x[PER - 1]);
-  else v = make_float4(x[0], x[1], __shfl_down_sync(0xffffffffu, x[0], 1), __shfl_down_sync(0xffffffffu, x[1], 1));
-  if (PER == 4 || !(lane & 1)) kv8a::write_out(f, b, t, h, lane * PER, v, mm, ll);
+  // through shared memory: the warps of a row, and 4 elements to a thread
+#pragma unroll
+  for (int d = 0; d < PER; ++d) s_x[warp][lane * PER + d] = x[d];
+  if (lane == 0) {
+    s_m[warp] = mm;
+    s_l[warp] = ll;
+  }
+  if (WPR > 1) __syncthreads();
+  else __syncwarp();
+  if (!live || sub || lane >= HD / 4) return;
+#pragma unroll
+  for (int w = 1; w < WPR; ++w) mm = fmaxf(mm, s_m[warp + w]);
+  const float base = mm == -INFINITY ? 0.f : mm;
+  float4 v = make_float4(0, 0, 0, 0);
+  ll = 0.f;
+#pragma unroll
+  for (int w = 0; w < WPR; ++w) {
+    const float4 y = *reinterpret_cast<const float4 *>(&s_x[warp + w][4 * lane]);
+    const float e = ex2(s_m[warp + w] - base);
+    v.x = fmaf(y.x, e, v.x); v.y = fmaf(y.y, e, v.y); v.z = fmaf(y.z, e, v.z); v.w = fmaf(y.w, e, v.w);
+    ll = fmaf(s_l[warp + w], e, ll);
+  }
+  kv8a::write_out(f, b, t, h, 4 * lane, v, mm, ll);
+}
+template <int HD>
+cudaError_t launch_join(const SharedArgs &a, const Kv8AttnArgs &f, const float *own, const float2 *raw, cudaStream_t s) {
+  const int64_t rows = (int64_t)a.B * a.T * a.H;
+  // four warps a row while the rows are few
+  if (rows <= 8192) return launch_k(k_shared_join<HD, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, s, 1, a, f, own, raw);
+  return launch_k(k_shared_join<HD, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, 1, a, f, own, raw);
 }
 
 struct Plan {
@@ -93,7 +132,7 @@ Plan plan_of(const Kv8 &cache, int B, int T, int fan, int H, int n_sm) {
   s.own_work = at; at += up(kv8_attention_work(cache, B, T, H, n_sm));
   s.own_out = at; at += up((size_t)B * T * H * cache.hd * 4);
   s.raw = at; at += up((size_t)B * T * H * 8);
-  s.line = at; at += up((size_t)(s.P + 2) * 8);
+  s.line = at; at += up((size_t)(s.P + 1) * 4);
   s.slots = at; at += up((size_t)(n_sm + s.units) * slot_floats(s.slot_rows, cache.hd) * 4);
   s.bytes = at + 240;  // the parts begin on 256-byte boundaries of a 16-byte aligned workspace
   return s;
@@ -112,6 +151,10 @@ int check_shared(const rv_kv8 *prefix, const rv_kv8 *cache, int B, int T, int fa
   if ((B + (int64_t)fan - 1) / fan > prefix->max_batch) return op_fail(RV_EINVAL, "B / fan above the prefix's max_batch");
   if (heads < 1 || heads > 65535 || heads % cache->n_kv_heads) return op_fail(RV_EINVAL, "query heads must be a multiple of n_kv_heads");
   if ((int64_t)B * T * heads > INT32_MAX / 8) return op_fail(RV_EINVAL, "B x T x heads above 2^28");
+  // what the kernels count in 32 bits: tiles of all units
+  const int64_t f = fan < B ? fan : B, rows = f * T * (heads / cache->n_kv_heads), tiles = ((int64_t)prefix->max_seq + kTile - 1) / kTile;
+  if ((B + f - 1) / f * cache->n_kv_heads * ((rows + kRows - 1) / kRows) * tiles > INT32_MAX / 2)
+    return op_fail(RV_EINVAL, "B / fan x n_kv_heads x the prefix's max_seq too large");
   return RV_OK;
 }
 
@@ -179,7 +222,7 @@ extern "C" int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache
   a.rows = plan.rows; a.groups = plan.groups; a.slot_rows = plan.slot_rows;
   a.scale = scale;
   a.plen = d_prefix_len; a.count = d_count; a.err = d_err;
-  a.line = reinterpret_cast<int64_t *>(work + plan.line);
+  a.line = reinterpret_cast<int32_t *>(work + plan.line);
   a.slots = reinterpret_cast<float *>(work + plan.slots);
   a.lo = c.act == RV_F16 || out->dtype == RV_F32;
   const cudaError_t e = a.c.fmt == RV_KV8_INT8 ? kv8s::launch_prefix_int8(a, n_sm, s) : kv8s::launch_prefix_e4m3(a, n_sm, s);
@@ -191,8 +234,6 @@ extern "C" int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache
   f.round_out = 0;
   f.raw = nullptr;
   f.lse = d_lse;
-  const dim3 grid((unsigned)(((int64_t)B * T * own.H + 7) / 8));
   const float *own_out = static_cast<const float *>(own.out.p);
-  return launched("rv_kv8_attention_shared", launch_k(c.hd == 64 ? kv8s::k_shared_join<64> : kv8s::k_shared_join<128>, grid, dim3(256), 0, s, 1, a, f,
-                                                      own_out, (const float2 *)own.raw));
+  return launched("rv_kv8_attention_shared", c.hd == 64 ? kv8s::launch_join<64>(a, f, own_out, own.raw, s) : kv8s::launch_join<128>(a, f, own_out, own.raw, s));
 }
