@@ -32,12 +32,15 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
   return ok != 0;
 }
 // Until the barrier's phase of this parity is done, or the limit is over, or
-// *dead (if not NULL) is set: false.
+// *dead (if not NULL) is set: false.  NAP: nanoseconds between tries, for those
+// who have time: warps that poll take issue slots of those that work.
+template <int NAP = 0>
 __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *dead = nullptr) {
 #pragma unroll 1
   for (uint32_t i = 0; i < kTries; ++i) {
     if (bar_try(b, parity)) return true;
     if (dead && *dead) return false;
+    if (NAP) __nanosleep(NAP);
   }
   return false;
 }

@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   const int lb = __ffs(c.block) - 1;
   volatile int *dead = &side.dead;
   // Waits are for whole warps.
-  auto wait = [&](uint64_t *b, uint32_t parity) {
-    const bool ok = __all_sync(0xffffffffu, bar_wait(b, parity, dead));
+  auto waited = [&](bool mine) {
+    const bool ok = __all_sync(0xffffffffu, mine);
     if (!ok) {
       if (!*dead && a.err) atomicOr(a.err, kErrWait);
       *dead = 1;
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
     __syncwarp();
     return ok;
   };
+  auto wait = [&](uint64_t *b, uint32_t parity) { return waited(bar_wait(b, parity, dead)); };
   // Tensor memory: the streams' scores (and weights), then their O.
   auto at_s = [&](int s) { return tmem + 128 * s; };
   auto at_o = [&](int s) { return tmem + 256 + HD * s; };
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         more = walk.next(a, part);
         t = part.t0;
       }
-      if (!wait(&bar.free[which][st], ((k >> 1) & 1) ^ 1)) break;
+      if (!waited(bar_wait<100>(&bar.free[which][st], ((k >> 1) & 1) ^ 1, dead))) break;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int off = st * TB + (HD == 128 ? j & 1 : 0) * kHalf + 32 * 128 * (HD == 128 ? j >> 1 : j);
@@ -498,37 +499,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           // Weights.  Scores are taken by their factor and off the reference in one step; where they are so large that
           // the reference's own rounding would be more than a quarter, the product is rounded first, as the reference was.
           const bool large = __any_sync(0xffffffffu, fabsf(m) > 4194304.f);
-#pragma unroll 1
-          for (int ch = 0; ch < 128; ch += 32) {
-            uint32_t v[32];
-            tmem_load32(my_s + ch, v);
-            tmem_wait_load(v);
-#pragma unroll 1
-            for (int turn = large; turn > 0; --turn) {
+          // a chunk of 32 positions: its scores, scaled by f and off the reference, become weights
+          auto weigh = [&](int ch, uint32_t (&v)[32], const F2 (&f)[2], int have) {
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const float f = factor(ch + 16 * h);
-#pragma unroll
-                for (int k = 16 * h; k < 16 * h + 16; ++k) v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]), f));
-              }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float f0 = factor(ch + 16 * h), f = large ? 1.f : f0;
-              const F2 ff = f2(f, f);
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
               for (int k = 16 * h; k < 16 * h + 16; k += 2) {
-                const float2 w = f2_split(f2_fma(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), ff, neg));
+                const float2 w = f2_split(f2_fma(f2(__uint_as_float(v[k]), __uint_as_float(v[k + 1])), f[h], neg));
                 v[k] = __float_as_uint(ex2(w.x));
                 v[k + 1] = __float_as_uint(ex2(w.y));
+                if (have < 32) {  // what is not there weighs nothing, whatever its scale
+                  if (k >= have) v[k] = 0;
+                  if (k + 1 >= have) v[k + 1] = 0;
+                }
               }
-            }
-#pragma unroll 1
-            for (int turn = ch + 32 > edge; turn > 0; --turn) {  // what is not there weighs nothing, whatever its scale
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (ch + k >= edge) v[k] = 0;
-            }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               const float vr = __shfl_sync(0xffffffffu, sc, 8 + ((ch + 16 * h) >> lb)) * unit;
@@ -547,6 +531,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
               }
               tmem_store8(my_s + ch + 8 * h, y);
               if (LO) tmem_store8(my_s + ch + 16 + 8 * h, z);
+            }
+          };
+          if (edge >= kTile && !large) {
+#pragma unroll 1
+            for (int ch = 0; ch < 128; ch += 32) {
+              uint32_t v[32];
+              tmem_load32(my_s + ch, v);
+              const float f0 = factor(ch), f1 = factor(ch + 16);
+              const F2 f[2] = {f2(f0, f0), f2(f1, f1)};
+              tmem_wait_load(v);
+              weigh(ch, v, f, 32);
+            }
+          } else {  // (apart: branches inside would keep the exponentials and the rest from running side by side, 364 cycles a chunk against 276)
+#pragma unroll 1
+            for (int ch = 0; ch < 128; ch += 32) {
+              uint32_t v[32];
+              tmem_load32(my_s + ch, v);
+              float f0 = factor(ch), f1 = factor(ch + 16);
+              tmem_wait_load(v);
+              if (large) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__fmul_rn(__uint_as_float(v[k]), k < 16 ? f0 : f1));
+                f0 = f1 = 1.f;
+              }
+              const F2 f[2] = {f2(f0, f0), f2(f1, f1)};
+              weigh(ch, v, f, edge - ch);
             }
           }
           tmem_wait_store();
