@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
   __shared__ int s_row;
   pdl_wait();
+  if (CL && a.raw) pdl_trigger();  // what comes next does not need this one's results before its end
   const Kv8 &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
   const int grp = a.H / c.Hkv, groups = (a.T * grp + ROWS - 1) / ROWS;

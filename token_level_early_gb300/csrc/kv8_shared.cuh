@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, side.tmem, 0);
-  pdl_wait();
+  // (no wait for the kernel before: it reads other positions, and all that this one reads or overwrites was done before it began)
   const Piece piece = cut_line<kThreads>(a, side.scratch);
   Walk walk{piece.begin, piece.end, piece.off, piece.p, piece.n};
   const Kv8 &c = a.c;
@@ -370,32 +370,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       float rf;
       {
         // the warp's rows as they are into their place, whole rows at a time; then each thread turns its own
-        constexpr int LR = HD / 8, RI = 32 / LR, NI = 8;  // lanes of a row, rows of a turn, turns at once
+        constexpr int LR = HD / 8, RI = 32 / LR, NI = 32 / RI;  // lanes of a row, rows of a turn, turns
         const int piece = lane % LR;
-#pragma unroll 1
-        for (int k0 = 0; k0 < 32; k0 += NI * RI) {
-          uint4 y[NI];
+        if (a.q_f32) {
+#pragma unroll 4
+          for (int k = 0; k < NI; ++k) {
+            const int64_t o = __shfl_sync(0xffffffffu, my_q, k * RI + lane / LR);
+            float4 u = make_float4(0, 0, 0, 0), v = u;
+            if (o >= 0) {
+              u = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + o + 8 * piece);
+              v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + o + 8 * piece + 4);
+            }
+            *q_piece(quarter * 32 + k * RI + lane / LR, piece) =
+                make_uint4(pack_act2(u.x, u.y, c.act), pack_act2(u.z, u.w, c.act), pack_act2(v.x, v.y, c.act), pack_act2(v.z, v.w, c.act));
+          }
+        } else {
+          uint4 y[NI];  // all on their way at once: behind the first tiles' codes, which every block asks for now, each turn would wait some 2 us
 #pragma unroll
           for (int k = 0; k < NI; ++k) {
-            const int64_t o = __shfl_sync(0xffffffffu, my_q, k0 + k * RI + lane / LR);
+            const int64_t o = __shfl_sync(0xffffffffu, my_q, k * RI + lane / LR);
             y[k] = make_uint4(0, 0, 0, 0);
-            if (o >= 0 && !a.q_f32) y[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + o + 8 * piece);
-          }
-          if (a.q_f32) {
-#pragma unroll 1
-            for (int k = 0; k < NI; ++k) {
-              const int64_t o = __shfl_sync(0xffffffffu, my_q, k0 + k * RI + lane / LR);
-              if (o < 0) continue;
-              const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + o + 8 * piece);
-              const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q.p) + o + 8 * piece + 4);
-              *q_piece(quarter * 32 + k0 + k * RI + lane / LR, piece) =
-                  make_uint4(pack_act2(u.x, u.y, c.act), pack_act2(u.z, u.w, c.act), pack_act2(v.x, v.y, c.act), pack_act2(v.z, v.w, c.act));
-            }
-            __syncwarp();
+            if (o >= 0) y[k] = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.q.p) + o + 8 * piece);
           }
 #pragma unroll
-          for (int k = 0; k < NI; ++k)
-            if (!a.q_f32 || __shfl_sync(0xffffffffu, my_q, k0 + k * RI + lane / LR) < 0) *q_piece(quarter * 32 + k0 + k * RI + lane / LR, piece) = y[k];
+          for (int k = 0; k < NI; ++k) *q_piece(quarter * 32 + k * RI + lane / LR, piece) = y[k];
         }
         __syncwarp();
         uint32_t top = 0;
@@ -624,6 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
     }
   }
   pdl_trigger();
+  pdl_wait();  // the join, which waits for this kernel, needs the one before too
   tmem_fence_before();
   __syncthreads();
   if (warp == kSoftWarps + kCodeWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
