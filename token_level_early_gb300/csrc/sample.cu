@@ -621,10 +621,13 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
   if (small)  // to the block that has the place
     asm volatile("red.relaxed.cluster.shared::cluster.add.u64 [%0], %1;" ::"r"(at_rank(&sh->small, values.mid / per_block)), "l"(small) : "memory");
   r.sync();
-  u64 n[MOST], w[MOST], mine[2] = {0, 0}, at[2], all[2];
+  uint32_t n[MOST];
+  u64 one[MOST], mine[2] = {0, 0}, at[2], all[2];  // weight of an element of a place; of mid: of all its elements
+  const auto mass = [&](int j) { return q0 + j == values.mid ? one[j] : n[j] * one[j]; };
 #pragma unroll
   for (int j = 0; j < MOST; ++j) {
-    n[j] = w[j] = 0;
+    n[j] = 0;
+    one[j] = 0;
     if (j < run) {
       uint32_t x[kMaxCluster];
 #pragma unroll
@@ -632,10 +635,10 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
 #pragma unroll
       for (int i = 0; i < kMaxCluster; ++i) n[j] += x[i];
       const float v = values.value(q0 + j);
-      if (n[j]) w[j] = q0 + j == values.mid ? sh->small : v >= bottom ? n[j] * weight(v, kept.s, kept.table) : 0;
+      if (n[j]) one[j] = q0 + j == values.mid ? sh->small : v >= bottom ? weight(v, kept.s, kept.table) : 0;
     }
     mine[0] += n[j];
-    mine[1] += w[j];
+    mine[1] += mass(j);
   }
   r.scan(mine, at, all);
   // the border: a value's place, how many of its elements stay, whether all do
@@ -652,17 +655,17 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
         r.tell(1, (uint32_t)(q0 + j));
         r.tell(2, (uint32_t)(left == n[j]));
         r.tell(0, left);
-        r.tell(1, b + (left == n[j] ? w[j] : w[j] / n[j] * left));  // (all of a place weigh the same, but the small ones)
+        r.tell(1, b + left * one[j]);
       }
       c += n[j];
-      b += w[j];
+      b += mass(j);
     }
     r.sync();
     edge = sh->found[1];
     every = sh->found[2] != 0;
     stay = sh->before[0];
     total = sh->before[1];
-    if ((int)edge == values.mid) return false;
+    if ((int)edge == values.mid) return false;  // (its weights differ)
   }
   if (p < 1.f) {
     const u64 goal = goal_of(p, total);
@@ -670,22 +673,20 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
 #pragma unroll
     for (int j = 0; j < MOST; ++j) {
       const uint32_t q = q0 + j;
-      const u64 one = n[j] ? w[j] / n[j] : 0, here = q < edge ? w[j] : q == edge ? (every ? w[j] : one * stay) : 0;
+      const u64 here = q < edge ? mass(j) : q == edge ? one[j] * (every ? (u64)n[j] : stay) : 0;
       if (b < goal && goal <= b + here) {
-        const u64 left = (goal - b + one - 1) / one;
+        const u64 left = (goal - b + one[j] - 1) / one[j];
         r.tell(3, q);
         r.tell(4, (uint32_t)(left == n[j]));
         r.tell(2, left);
       }
-      b += w[j];
+      b += mass(j);
     }
     r.sync();
     edge = sh->found[3];
     every = sh->found[4] != 0;
     stay = sh->before[2];
-    if ((int)edge == values.mid) return false;  // (its weights differ)
-  } else {
-    r.sync();  // the counts have been read
+    if ((int)edge == values.mid) return false;
   }
   // ---- a weight for each place; elements at the border count in units of 2^52
   constexpr u64 TIE = 1ull << 52;
@@ -696,10 +697,11 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
   }
   __syncthreads();
   const bool small_stay = values.mid >= 0 && values.mid < (int)edge;
+  const uint32_t last = min(edge, (uint32_t)kSteps - 1);
   u64 mixed = 0;
   r.each_bits([&](uint16_t bits, int) {
     const uint32_t q = values.place(bits);
-    if (q >= (uint32_t)kSteps) return;
+    if (q > last) return;
     mixed += sh->value[q];
     if ((int)q == values.mid && small_stay) {
       const float x = __uint_as_float((uint32_t)bits << 16);
