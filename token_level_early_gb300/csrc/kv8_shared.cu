@@ -13,10 +13,11 @@ namespace kv8s {
 
 // ------------------------------------------------------------------ join
 
-// WPR warps an output row: the prefix's parts, up to kJoin of them on their way
-// at once, and the own positions' state.  What this takes is the latency of its
-// dependent loads where rows are few, and reading the states where they are many.
-constexpr int kJoin = 5;
+// A warp an output row: the prefix's parts, kJoin of them on their way at once,
+// and the own positions' state.  (Measured with 5 and 10 at once, and with 2 or
+// 4 warps a row: 72.7, 71.9, 73.3 and 73.5 us of the whole for 64 rows behind
+// 32K positions, 55.2, 56.0, 58.7 and 60.1 for 16 prompts of 8 rows.)
+constexpr int kJoin = 8;
 template <int PER>
 __device__ __forceinline__ void load_part(float (&x)[PER], const float *from) {
   if (PER == 4) {
@@ -27,91 +28,60 @@ __device__ __forceinline__ void load_part(float (&x)[PER], const float *from) {
     x[0] = v.x; x[1] = v.y;
   }
 }
-template <int HD, int WPR>
+template <int HD>
 __global__ void __launch_bounds__(256) k_shared_join(const __grid_constant__ SharedArgs a, const __grid_constant__ Kv8AttnArgs f, const float *own,
                                                      const float2 *raw) {
   constexpr int PER = HD / 32;
-  __shared__ __align__(16) float s_x[8][HD];
-  __shared__ float s_m[8], s_l[8];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-  const int row = blockIdx.x * (8 / WPR) + warp / WPR, bt = row / a.H, h = row - bt * a.H, b = bt / a.T, t = bt - b * a.T;
-  const bool live = row < a.B * a.T * a.H && t < row_count(a.count, b, a.T);
-  float mm = -INFINITY, ll = 0.f, x[PER];
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), bt = row / a.H, h = row - bt * a.H, b = bt / a.T, t = bt - b * a.T;
+  if (row >= a.B * a.T * a.H || t >= row_count(a.count, b, a.T)) return;
+  const int grp = a.H / a.c.Hkv, p = b / a.fan, g = h / grp, i = ((b - p * a.fan) * a.T + t) * grp + h - g * grp, group = i / kRows, rr = i - group * kRows;
+  const int tiles = prefix_tiles(a, p), piece = a.line[a.P], begin = a.line[p] + (g * a.groups + group) * tiles;
+  const float2 s0 = raw[row];
+  float mm = s0.y == 0.f ? -INFINITY : s0.x, ll = s0.y, x[PER];
+  load_part(x, own + (int64_t)row * HD + lane * PER);
+  const int c0 = begin / piece, c1 = tiles ? (begin + tiles - 1) / piece : -1;
+  const float *slots = a.slots + (size_t)((p * a.c.Hkv + g) * a.groups + group) * slot_floats(a.slot_rows, HD);
+  for (int c = c0; c <= c1; c += kJoin) {
+    float2 v[kJoin];
+    float y[kJoin][PER], top = mm;
 #pragma unroll
-  for (int d = 0; d < PER; ++d) x[d] = 0.f;
-  if (live) {
-    const int grp = a.H / a.c.Hkv, p = b / a.fan, g = h / grp, i = ((b - p * a.fan) * a.T + t) * grp + h - g * grp, group = i / kRows, rr = i - group * kRows;
-    const int tiles = prefix_tiles(a, p), piece = a.line[a.P], begin = a.line[p] + (g * a.groups + group) * tiles;
-    if (sub == 0) {
-      const float2 v = raw[row];
-      mm = v.y == 0.f ? -INFINITY : v.x;
-      ll = v.y;
-      load_part(x, own + (int64_t)row * HD + lane * PER);
-    }
-    const int c0 = begin / piece, c1 = tiles ? (begin + tiles - 1) / piece : -1;
-    const float *slots = a.slots + (size_t)((p * a.c.Hkv + g) * a.groups + group) * slot_floats(a.slot_rows, HD);
-    for (int c = c0 + sub; c <= c1; c += kJoin * WPR) {
-      float2 v[kJoin];
-      float y[kJoin][PER], top = mm;
+    for (int j = 0; j < kJoin; ++j) {
+      v[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-      for (int j = 0; j < kJoin; ++j) {
-        v[j] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-        for (int d = 0; d < PER; ++d) y[j][d] = 0.f;
-        if (c + j * WPR <= c1) {
-          const float *s = slots + (size_t)(c + j * WPR) * slot_floats(a.slot_rows, HD);
-          v[j] = *reinterpret_cast<const float2 *>(s + (size_t)a.slot_rows * HD + 2 * rr);
-          load_part(y[j], s + (size_t)rr * HD + lane * PER);
-        }
+      for (int d = 0; d < PER; ++d) y[j][d] = 0.f;
+      if (c + j <= c1) {
+        const float *s = slots + (size_t)(c + j) * slot_floats(a.slot_rows, HD);
+        v[j] = *reinterpret_cast<const float2 *>(s + (size_t)a.slot_rows * HD + 2 * rr);
+        load_part(y[j], s + (size_t)rr * HD + lane * PER);
       }
-#pragma unroll
-      for (int j = 0; j < kJoin; ++j) top = fmaxf(top, v[j].x);
-      const float base = top == -INFINITY ? 0.f : top, old = ex2(mm - base);
-      ll *= old;
-#pragma unroll
-      for (int d = 0; d < PER; ++d) x[d] *= old;
-#pragma unroll
-      for (int j = 0; j < kJoin; ++j) {
-        const float e = ex2(v[j].x - base);
-        ll = fmaf(v[j].y, e, ll);
-#pragma unroll
-        for (int d = 0; d < PER; ++d) x[d] = fmaf(y[j][d], e, x[d]);
-      }
-      mm = top;
     }
-  }
-  // through shared memory: the warps of a row, and 4 elements to a thread
 #pragma unroll
-  for (int d = 0; d < PER; ++d) s_x[warp][lane * PER + d] = x[d];
-  if (lane == 0) {
-    s_m[warp] = mm;
-    s_l[warp] = ll;
-  }
-  if (WPR > 1) __syncthreads();
-  else __syncwarp();
-  if (!live || sub || lane >= HD / 4) return;
+    for (int j = 0; j < kJoin; ++j) top = fmaxf(top, v[j].x);
+    const float base = top == -INFINITY ? 0.f : top, old = ex2(mm - base);
+    ll *= old;
 #pragma unroll
-  for (int w = 1; w < WPR; ++w) mm = fmaxf(mm, s_m[warp + w]);
-  const float base = mm == -INFINITY ? 0.f : mm;
-  float4 v = make_float4(0, 0, 0, 0);
-  ll = 0.f;
+    for (int d = 0; d < PER; ++d) x[d] *= old;
 #pragma unroll
-  for (int w = 0; w < WPR; ++w) {
-    const float4 y = *reinterpret_cast<const float4 *>(&s_x[warp + w][4 * lane]);
-    const float e = ex2(s_m[warp + w] - base);
-    v.x = fmaf(y.x, e, v.x); v.y = fmaf(y.y, e, v.y); v.z = fmaf(y.z, e, v.z); v.w = fmaf(y.w, e, v.w);
-    ll = fmaf(s_l[warp + w], e, ll);
+    for (int j = 0; j < kJoin; ++j) {
+      const float e = ex2(v[j].x - base);
+      ll = fmaf(v[j].y, e, ll);
+#pragma unroll
+      for (int d = 0; d < PER; ++d) x[d] = fmaf(y[j][d], e, x[d]);
+    }
+    mm = top;
   }
-  kv8a::write_out(f, b, t, h, 4 * lane, v, mm, ll);
+  float4 v;
+  if (PER == 4) v = make_float4(x[0], x[1], x[PER - 2], x[PER - 1]);
+  else v = make_float4(x[0], x[1], __shfl_down_sync(0xffffffffu, x[0], 1), __shfl_down_sync(0xffffffffu, x[1], 1));
+  if (PER == 4 || !(lane & 1)) kv8a::write_out(f, b, t, h, lane * PER, v, mm, ll);
 }
 template <int HD>
 cudaError_t launch_join(const SharedArgs &a, const Kv8AttnArgs &f, const float *own, const float2 *raw, cudaStream_t s) {
   const int64_t rows = (int64_t)a.B * a.T * a.H;
-  // four warps a row while the rows are few
-  if (rows <= 8192) return launch_k(k_shared_join<HD, 4>, dim3((unsigned)((rows + 1) / 2)), dim3(256), 0, s, 1, a, f, own, raw);
-  return launch_k(k_shared_join<HD, 1>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, 1, a, f, own, raw);
+  return launch_k(k_shared_join<HD>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, 1, a, f, own, raw);
 }
 
 struct Plan {

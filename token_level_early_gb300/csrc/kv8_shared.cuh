@@ -12,8 +12,13 @@
 // A block per SM: 4 warps turn K codes to fp16 and 4 V codes, one thread issues
 // the products, 8 warps in two streams do the softmax, so that one's products run under the
 // other's weights.  Up to 128 query rows, the streams take every other tile of
-// positions and are joined at the end; with more, each has its 128 rows.
+// positions and are joined at the end; with more, each has its 128 rows.  With 32
+// or 64 rows at most, the rows are there four times or twice, each time for
+// another part of a tile's positions (the others' weights are zero): the products
+// would take as long with empty rows, and so all warps share the weights.
 #pragma once
+
+#include <type_traits>
 
 #include "async.cuh"
 #include "kv8_attention.cuh"
@@ -356,16 +361,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
     const uint32_t lanes = (uint32_t)quarter << 21;  // the warp's first lane, in an address
     const uint32_t my_s = at_s(s) + lanes, my_o = at_o(s) + lanes;
     const int grp = a.H / c.Hkv, nb = kTile >> lb;  // blocks of a tile: their K scales in lanes 0.., their V scales in lanes 8..
-    uint32_t items = 0, parts = 0, outs = 0;
+    uint32_t items = 0, outs = 0, exchanges = 0;
     bool ok = true;
     while (ok && walk.next(a, part)) {
       const bool two = part.rows > 128;
       const int per = two ? 1 : 2, tiles = part.t1 - part.t0;  // tiles from one item of the stream to its next
       // ---- queries, scaled by a power of two into fp16's range
-      const int row0 = part.group * kRows + (two ? 128 * s : 0), end = part.group * kRows + part.rows;
-      const QueryRow qr = query_row(a, part.p, row0 + r, grp);
-      const bool live = row0 + r < end && qr.live;
-      const int64_t my_q = live ? qr.b * a.q.sb + qr.t * a.q.st + (part.g * grp + (row0 + r) % grp) * a.q.sh : -1;
+      const int times = two || part.rows > 64 ? 1 : part.rows > 32 ? 2 : 4, span = kTile / times;  // copies of the rows, positions of each
+      const int i_row = r & (span - 1), copy = r / span, row0 = part.group * kRows + (two ? 128 * s : 0), end = part.group * kRows + part.rows;
+      const QueryRow qr = query_row(a, part.p, row0 + i_row, grp);
+      const bool live = row0 + i_row < end && qr.live;
+      const int64_t my_q = live ? qr.b * a.q.sb + qr.t * a.q.st + (part.g * grp + (row0 + i_row) % grp) * a.q.sh : -1;
       auto q_piece = [&](int row, int k) { return reinterpret_cast<uint4 *>(sq + s * TB + row * 128 + (k >> 3) * kHalf + (((k & 7) ^ (row & 7)) << 4)); };
       float rf;
       {
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         }
         __syncwarp();
         uint32_t top = 0;
-#pragma unroll 2
+#pragma unroll 4
         for (int k = 0; k < HD / 8; ++k) {
           const uint4 y = *q_piece(r, k);
           top = max_magnitude(max_magnitude(max_magnitude(max_magnitude(top, y.x), y.y), y.z), y.w);
@@ -408,18 +414,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         const int e = max(min((int)(__float_as_uint(mx) >> 23), 254) - 127, QE - 126);
         const float down = copysignf(__uint_as_float((uint32_t)(127 + QE - e) << 23), a.scale);  // the scale's sign goes to the query
         rf = mx < INFINITY ? __uint_as_float((uint32_t)(127 + e - QE) << 23) * fabsf(a.scale) * kLog2e : __int_as_float(0x7fc00000);
-#pragma unroll 2
-        for (int k = 0; k < HD / 8; ++k) {
-          const uint4 y = *q_piece(r, k);
-          auto scaled = [&](uint32_t w) { return kv8a::pack_h2(act_to_f((uint16_t)w, c.act) * down, act_to_f((uint16_t)(w >> 16), c.act) * down); };
-          *q_piece(r, k) = make_uint4(scaled(y.x), scaled(y.y), scaled(y.z), scaled(y.w));
-        }
+        auto turn = [&](auto bf16) {
+#pragma unroll 4
+          for (int k = 0; k < HD / 8; ++k) {
+            const uint4 y = *q_piece(r, k);
+            auto scaled = [&](uint32_t w) {
+              if (decltype(bf16)::value) return kv8a::pack_h2(__uint_as_float(w << 16) * down, __uint_as_float(w & 0xffff0000u) * down);
+              const float2 v = __half22float2(kv8a::bits_h2(w));
+              return kv8a::pack_h2(v.x * down, v.y * down);
+            };
+            *q_piece(r, k) = make_uint4(scaled(y.x), scaled(y.y), scaled(y.z), scaled(y.w));
+          }
+        };
+        if (c.act == RV_BF16) turn(std::true_type{});
+        else turn(std::false_type{});
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) bar_arrive(&bar.q_full[s]);
-      ++parts;
       // ---- items
+      const int from = copy * span, to = from + span;   // this row's positions of a tile
       const bool some = __any_sync(0xffffffffu, live);  // rows that no one asks for need no weights
       float m = kv8a::kUnseen, scales = 0.f;
       F2 l[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
@@ -448,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           // the row's largest score
           float top = -INFINITY;
 #pragma unroll 1
-          for (int ch = 0; ch < 128; ch += 32) {
+          for (int ch = from; ch < to; ch += 32) {
             uint32_t x[32];
             tmem_load32(my_s + ch, x);
             tmem_wait_load(x);
@@ -473,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           if (ve > 128) ve = -200;  // NaN
           ve = __reduce_max_sync(0xffffffffu, ve);
           if (__any_sync(0xffffffffu, top - m > kv8a::kLag) || ve > e) {
-            const float to = top - m > kv8a::kLag ? top - kv8a::kTop : m, al = ex2(m - to);
+            const float next = top - m > kv8a::kLag ? top - kv8a::kTop : m, al = ex2(m - next);
             const int en = max(e, ve);
             l[0] = f2_mul(l[0], f2(al, al));
             l[1] = f2_mul(l[1], f2(al, al));
@@ -489,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
                 tmem_store32(my_o + 32 * ch, x);
               }
             }
-            m = to;
+            m = next;
             e = en;
           }
           const float unit = __uint_as_float((uint32_t)min(max(127 - e, 1), 254) << 23);  // 2^-e
@@ -531,9 +545,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
               if (LO) tmem_store8(my_s + ch + 16 + 8 * h, z);
             }
           };
+          if (times > 1) {  // other copies' positions
+            const uint32_t none[8] = {};
+            for (int ch = 0; ch < kTile; ch += 32)
+              if (ch < from || ch >= to) {
+                tmem_store8(my_s + ch, none);
+                tmem_store8(my_s + ch + 8, none);
+                if (LO) {
+                  tmem_store8(my_s + ch + 16, none);
+                  tmem_store8(my_s + ch + 24, none);
+                }
+              }
+          }
           if (edge >= kTile && !large) {
 #pragma unroll 1
-            for (int ch = 0; ch < 128; ch += 32) {
+            for (int ch = from; ch < to; ch += 32) {
               uint32_t v[32];
               tmem_load32(my_s + ch, v);
               const float f0 = factor(ch), f1 = factor(ch + 16);
@@ -543,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
             }
           } else {  // (apart: branches inside would keep the exponentials and the rest from running side by side, 364 cycles a chunk against 276)
 #pragma unroll 1
-            for (int ch = 0; ch < 128; ch += 32) {
+            for (int ch = from; ch < to; ch += 32) {
               uint32_t v[32];
               tmem_load32(my_s + ch, v);
               float f0 = factor(ch), f1 = factor(ch + 16);
@@ -576,18 +602,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&bar.exchange);
-      ok = wait(&bar.exchange, (parts - 1) & 1);
+      ok = wait(&bar.exchange, exchanges++ & 1);
       if (!ok) break;
       tmem_fence_after();
       float *slot = a.slots + part.slot * slot_floats(a.slot_rows, HD);
       float *ml = slot + (size_t)a.slot_rows * HD;
       auto power = [&](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
       // O in units of 2^40 and of m's reference: the stream's own rows, or half of the elements of both streams' rows
-      const int other = two ? s : s ^ 1, rr = two ? 128 * s + r : r;
-      const float m0 = side.m[s][r], m1 = side.m[other][r], mm = fmaxf(m0, m1), f0 = ex2(m0 - mm), f1 = ex2(m1 - mm);
-      const float g0 = f0 * power(side.e[s][quarter]), g1 = f1 * power(side.e[other][quarter]);
+      const int other = two ? s : s ^ 1, rr = two ? 128 * s + r : i_row;
+      float mm = fmaxf(side.m[s][r], side.m[other][r]);
+      for (int k = 0; k < times; ++k) mm = fmaxf(mm, fmaxf(side.m[s][k * span + i_row], side.m[other][k * span + i_row]));
+      const float g0 = ex2(side.m[s][r] - mm) * power(side.e[s][quarter]), g1 = ex2(side.m[other][r] - mm) * power(side.e[other][quarter]);
       const bool others = !two && (s == 1 || tiles > 1);
       const int c0 = two ? 0 : s * (HD / 2), c1 = two ? HD : c0 + HD / 2;
+      // with copies: through the queries' place (a row HD / 2 numbers, 16-byte pieces by piece ^ (row mod 8)), and summed
+      auto put = [&](int row, int k) { return reinterpret_cast<float4 *>(sq + s * TB + row * (HD * 2) + ((k ^ (row & 7)) << 4)); };
 #pragma unroll 1
       for (int at = c0; at < c1; at += 32) {
         uint32_t x[32];
@@ -607,7 +636,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(fmaf(__uint_as_float(y[k]) * (1.f / kOutUnit), g1, __uint_as_float(x[k])));
         }
-        if (live) {
+        if (times > 1) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *put(r, (at - c0 + k) / 4) = make_float4(__uint_as_float(x[k]), __uint_as_float(x[k + 1]), __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+        } else if (live) {
           float *to = slot + (size_t)rr * HD + at;
 #pragma unroll
           for (int k = 0; k < 32; k += 8)
@@ -617,7 +650,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
         }
         __syncwarp();
       }
-      if (live && (two || s == 0)) *reinterpret_cast<float2 *>(ml + 2 * rr) = make_float2(mm, two ? side.l[s][r] : fmaf(side.l[0][r], f0, side.l[1][r] * f1));
+      if (live && copy == 0 && (two || s == 0)) {
+        float sum = 0.f;
+        for (int k = 0; k < times; ++k) {
+          sum = fmaf(side.l[s][k * span + i_row], ex2(side.m[s][k * span + i_row] - mm), sum);
+          if (!two) sum = fmaf(side.l[1][k * span + i_row], ex2(side.m[1][k * span + i_row] - mm), sum);
+        }
+        *reinterpret_cast<float2 *>(ml + 2 * rr) = make_float2(mm, sum);
+      }
+      if (times > 1) {
+        if (lane == 0) bar_arrive(&bar.exchange);
+        ok = wait(&bar.exchange, exchanges++ & 1);
+        if (!ok) break;
+        for (int k = r; k < part.rows * (HD / 8); k += 128) {
+          const int row = k / (HD / 8), piece = k % (HD / 8);
+          float4 x = *put(row, piece);
+          for (int t = 1; t < times; ++t) {
+            const float4 y = *put(t * span + row, piece);
+            x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          }
+          *reinterpret_cast<float4 *>(slot + (size_t)row * HD + c0 + 4 * piece) = x;  // (rows that no one asks for too: of the slot, and not read)
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar.exchange);
+        ok = wait(&bar.exchange, exchanges++ & 1);  // before the next queries take the place
+        if (!ok) break;
+      }
       tmem_fence_before();  // (the next part's products write what was read here)
     }
   }
