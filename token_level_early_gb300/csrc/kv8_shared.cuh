@@ -9,8 +9,8 @@
 // as fp16 (two terms for fp16 caches and fp32 outputs) from tensor memory, where
 // they take their scores' place.  O stays in tensor memory.
 //
-// A block per SM: 4 warps turn K codes to fp16 and 4 V codes, one thread issues
-// the products, 8 warps in two streams do the softmax, so that one's products run under the
+// A block per SM: 4 or 8 warps turn codes to fp16, one thread issues the
+// products, 8 warps in two streams do the softmax, so that one's products run under the
 // other's weights.  Up to 128 query rows, the streams take every other tile of
 // positions and are joined at the end; with more, each has its 128 rows.  With 32
 // or 64 rows at most, the rows are there four times or twice, each time for
@@ -79,7 +79,7 @@ __device__ __forceinline__ QueryRow query_row(const SharedArgs &a, int p, int i,
 
 // The line: this block's piece, and the prefix row that it begins in.  Every
 // block computes it; block 0 leaves it for the join.
-constexpr int kMinTiles = 2;  // of a piece
+constexpr int kMinTiles = 1;  // of a piece (2: 13.1 us instead of 12.1 behind 200 positions; 4: 20.8)
 struct Piece {
   int begin, end, off, p, n;  // off: into row p; n: its length, if known (else -1)
 };
@@ -131,8 +131,13 @@ __device__ __forceinline__ Piece cut_line(const SharedArgs &a, int *scratch /* T
 
 // ------------------------------------------------------------------ the prefix
 
-constexpr int kSoftWarps = 8, kCodeWarps = 8,  // (4 for K, 4 for V)
-               kThreads = 32 * (kSoftWarps + kCodeWarps + 1);
+constexpr int kSoftWarps = 8;
+// Warps that turn codes to fp16: 4 for K and V, or 4 for each where tiles are
+// short and follow one another sooner.  (4 / 8, with 128 / 96 registers a thread:
+// head_dim 128, 64 rows behind 32K positions 69.5 / 73.4 us; 64, 16 prompts of 8
+// rows 57.3 / 51.7.)
+__host__ __device__ constexpr int code_warps(int hd) { return hd == 128 ? 4 : 8; }
+__host__ __device__ constexpr int threads_of(int hd) { return 32 * (kSoftWarps + code_warps(hd) + 1); }
 constexpr int kHalf = 16384;  // 128 rows of 64 fp16
 __host__ __device__ constexpr int tile_bytes(int hd) { return hd / 64 * kHalf; }
 struct Bars {
@@ -145,7 +150,7 @@ struct Side {
   Bars bar;
   float m[2][128], l[2][128];
   int e[2][4];
-  int scratch[kThreads + 2];
+  int scratch[threads_of(64) + 2];
   uint32_t tmem;
   int dead;  // a wait ran out: everyone leaves
 };
@@ -202,10 +207,11 @@ __device__ __forceinline__ uint2 codes4(uint32_t w) {
 }
 
 template <int FMT, int HD, bool LO>
-__global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ SharedArgs a) {
+__global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_constant__ SharedArgs a) {
   extern __shared__ unsigned char raw[];
   unsigned char *sm = raw + (-smem_addr(raw) & 1023);  // (as an offset, so that the compiler knows it for shared memory)
-  constexpr int TB = tile_bytes(HD);
+  constexpr int TB = tile_bytes(HD), kCodeWarps = code_warps(HD);
+  constexpr bool APART = kCodeWarps == 8;  // K's and V's warps
   unsigned char *sq = sm, *sk = sm + 2 * TB, *sv = sm + 4 * TB;
   Side &side = *reinterpret_cast<Side *>(sm + 6 * TB);
   Bars &bar = side.bar;
@@ -216,9 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      bar_init(&bar.full[0][i], kCodeWarps / 2);
+      bar_init(&bar.full[0][i], 4);
       bar_init(&bar.free[0][i], 1);
-      bar_init(&bar.full[1][i], kCodeWarps / 2);
+      bar_init(&bar.full[1][i], 4);
       bar_init(&bar.free[1][i], 1);
       bar_init(&bar.q_full[i], kSoftWarps / 2);
       bar_init(&bar.s_full[i], 1);
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, side.tmem, 0);
   // (no wait for the kernel before: it reads other positions, and all that this one reads or overwrites was done before it began)
-  const Piece piece = cut_line<kThreads>(a, side.scratch);
+  const Piece piece = cut_line<threads_of(HD)>(a, side.scratch);
   Walk walk{piece.begin, piece.end, piece.off, piece.p, piece.n};
   const Kv8 &c = a.c;
   const int lb = __ffs(c.block) - 1;
@@ -262,42 +268,51 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
     // Thread: 16 codes of position 32 j + 8 w + lane / 4 of the tile, and 64 codes on; a phase of 8 lanes
     // reads 64 bytes of two positions and stores 16-byte pieces that meet all banks.
     constexpr int NC = HD / 16;  // 16-byte loads of a thread and tile
-    const int w = warp & 3, which = (warp - kSoftWarps) >> 2, p_in = 8 * w + (lane >> 2);
-    const uint8_t *codes = c.codes[which] + (lane & 3) * 16;
+    const int w = warp & 3, p_in = 8 * w + (lane >> 2);
     const int x = p_in & 7, piece = (lane & 3) * 2;
-    unsigned char *to0 = (which ? sv : sk) + p_in * 128 + ((piece ^ x) << 4), *to1 = (which ? sv : sk) + p_in * 128 + (((piece + 1) ^ x) << 4);
-    uint4 buf[NC];
-    auto load = [&](const Part &s, int t) {
+    unsigned char *to0 = sk + p_in * 128 + ((piece ^ x) << 4), *to1 = sk + p_in * 128 + (((piece + 1) ^ x) << 4);
+    constexpr int OPS = APART ? 1 : 2;  // K and V, or one of them
+    auto which_of = [&](int o) { return APART ? (warp - kSoftWarps) >> 2 : o; };
+    uint4 buf[OPS][NC];
+    auto load = [&](int o, const Part &s, int t) {
       const int p0 = t * kTile + p_in;
-      const uint8_t *from = codes + ((int64_t)s.kv * c.N + p0) * HD;
+      const uint8_t *from = c.codes[which_of(o)] + ((int64_t)s.kv * c.N + p0) * HD + (lane & 3) * 16;
 #pragma unroll
       for (int j = 0; j < NC; ++j) {
         const int half = HD == 128 ? j & 1 : 0, at = 32 * (HD == 128 ? j >> 1 : j);
-        buf[j] = make_uint4(0, 0, 0, 0);
-        if (p0 + at < s.n) buf[j] = *reinterpret_cast<const uint4 *>(from + at * HD + half * 64);
+        buf[o][j] = make_uint4(0, 0, 0, 0);
+        if (p0 + at < s.n) buf[o][j] = *reinterpret_cast<const uint4 *>(from + at * HD + half * 64);
       }
     };
-    bool more = walk.next(a, part);
-    if (more) load(part, part.t0);
+    bool more = walk.next(a, part), ok = true;
+    if (more)
+#pragma unroll
+      for (int o = 0; o < OPS; ++o) load(o, part, part.t0);
     int t = part.t0;
-    for (uint32_t k = 0; more; ++k) {
+    for (uint32_t k = 0; ok && more; ++k) {
       const uint32_t st = k & 1;
       if (++t == part.t1) {
         more = walk.next(a, part);
         t = part.t0;
       }
-      if (!waited(bar_wait<100>(&bar.free[which][st], ((k >> 1) & 1) ^ 1, dead))) break;
 #pragma unroll
-      for (int j = 0; j < NC; ++j) {
-        const int off = st * TB + (HD == 128 ? j & 1 : 0) * kHalf + 32 * 128 * (HD == 128 ? j >> 1 : j);
-        const uint2 y0 = codes4<FMT>(buf[j].x), y1 = codes4<FMT>(buf[j].y), y2 = codes4<FMT>(buf[j].z), y3 = codes4<FMT>(buf[j].w);
-        *reinterpret_cast<uint4 *>(to0 + off) = make_uint4(y0.x, y0.y, y1.x, y1.y);
-        *reinterpret_cast<uint4 *>(to1 + off) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+      for (int o = 0; o < OPS; ++o) {
+        const int which = which_of(o);
+        ok = ok && waited(bar_wait<100>(&bar.free[which][st], ((k >> 1) & 1) ^ 1, dead));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          const int off = which * 2 * TB + st * TB + (HD == 128 ? j & 1 : 0) * kHalf + 32 * 128 * (HD == 128 ? j >> 1 : j);
+          const uint4 b = buf[o][j];
+          const uint2 y0 = codes4<FMT>(b.x), y1 = codes4<FMT>(b.y), y2 = codes4<FMT>(b.z), y3 = codes4<FMT>(b.w);
+          *reinterpret_cast<uint4 *>(to0 + off) = make_uint4(y0.x, y0.y, y1.x, y1.y);
+          *reinterpret_cast<uint4 *>(to1 + off) = make_uint4(y2.x, y2.y, y3.x, y3.y);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar.full[which][st]);
+        if (more) load(o, part, t);
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&bar.full[which][st]);
-      if (more) load(part, t);
     }
   } else if (warp == kSoftWarps + kCodeWarps) {
     // ================================================ products
@@ -309,27 +324,30 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
     while (ok && walk.next(a, part)) {
       const int per = part.rows > 128 ? 2 : 1, n = (part.t1 - part.t0) * per;
       for (int s = 0; ok && s < 2; ++s) ok = wait(&bar.q_full[s], parts & 1);
+      auto tile_of = [&](int i) { return tiles + (per == 2 ? i >> 1 : i); };
+      auto there = [&](int which, int i) { return wait(&bar.full[which][tile_of(i) & 1], (tile_of(i) >> 1) & 1); };
       auto scores = [&](int i) {
         const int s = i & 1;
-        const uint32_t k = tiles + (per == 2 ? i >> 1 : i), st = k & 1;
-        ok = ok && wait(&bar.full[0][st], (k >> 1) & 1);
-        if (!ok) return;
-        tmem_fence_after();
+        const uint32_t st = tile_of(i) & 1;
         const uint64_t q = q_op + s * (TB >> 4), kk = k_op + st * (TB >> 4);
         const uint32_t d = at_s(s);
-        if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < HD / 16; ++j) mma_ss(d, q + (((j >> 2) * kHalf + (j & 3) * 32) >> 4), kk + (((j >> 2) * kHalf + (j & 3) * 32) >> 4), KIND_S, j != 0);
-          mma_commit(&bar.s_full[s]);
-          if (per == 1 || s == 1) mma_commit(&bar.free[0][st]);
-        }
-        __syncwarp();
+        for (int j = 0; j < HD / 16; ++j) mma_ss(d, q + (((j >> 2) * kHalf + (j & 3) * 32) >> 4), kk + (((j >> 2) * kHalf + (j & 3) * 32) >> 4), KIND_S, j != 0);
+        mma_commit(&bar.s_full[s]);
+        if (per == 1 || s == 1) mma_commit(&bar.free[0][st]);
       };
-      for (int i = 0; i < 2 && i < n; ++i) scores(i);
+      for (int i = 0; ok && i < 2 && i < n; ++i) {
+        ok = there(0, i);
+        if (!ok) break;
+        tmem_fence_after();
+        if (elect_one()) scores(i);
+        __syncwarp();
+      }
       for (int i = 0; ok && i < n; ++i) {
         const int s = i & 1;
-        const uint32_t k = tiles + (per == 2 ? i >> 1 : i), st = k & 1;
-        ok = wait(&bar.full[1][st], (k >> 1) & 1) && wait(&bar.p_full[s], (items >> s) & 1);
+        const uint32_t st = tile_of(i) & 1;
+        // (what is waited for last is what comes last: a wait takes some 200 cycles, done or not, and none lies between the two products)
+        ok = there(1, i) && (i + 2 >= n || there(0, i + 2)) && wait(&bar.p_full[s], (items >> s) & 1);
         if (!ok) break;
         items ^= 1u << s;
         tmem_fence_after();
@@ -343,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_prefix(const __grid_constant__ 
           }
           if (per == 1 || s == 1) mma_commit(&bar.free[1][st]);
           if (i + 2 >= n) mma_commit(&bar.o_full[s]);
+          else scores(i + 2);
         }
         __syncwarp();
-        if (i + 2 < n) scores(i + 2);
       }
       tiles += part.t1 - part.t0;
       ++parts;
@@ -691,7 +709,7 @@ cudaError_t launch_prefix_t(const SharedArgs &a, int n_sm, cudaStream_t s) {
   auto fn = k_prefix<FMT, HD, LO>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, prefix_smem(HD));
   if (e != cudaSuccess) return e;
-  return launch_k(fn, dim3(n_sm), dim3(kThreads), prefix_smem(HD), s, 1, a);
+  return launch_k(fn, dim3(n_sm), dim3(threads_of(HD)), prefix_smem(HD), s, 1, a);
 }
 template <int FMT>
 cudaError_t launch_prefix_fmt(const SharedArgs &a, int n_sm, cudaStream_t s) {
