@@ -160,3 +160,47 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert ids.cpu().tolist() == [draw(r, float(np.float32(0.8)), 0, float(np.float32(0.9)), 0.0, float(np.float32(w)))[0]
                                       for r, w in zip(y.double().cpu().tolist(), v)]
+
+
+def spaced(seed, B, V, centre, spread, dtype=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(B, V, generator=g) * spread + centre).to(dtype).cuda()
+
+
+@pytest.mark.parametrize("centre,spread,t", [
+    (-8.0, 1.5, 0.8), (0.0, 0.003, 0.001), (0.0, 0.003, 1.0), (0.001, 0.004, 0.002), (-0.02, 0.006, 0.01), (300.0, 40.0, 20.0), (0.0, 2000.0, 300.0),
+    (-1e-3, 1e-4, 1.0), (0.0, 1e-30, 1e-30), (3.0, 0.02, 0.01)])
+def test_bf16_values_small_large_and_of_one_sign(centre, spread, t):
+    """Values share few numbers; the ones next to zero share a place, where the
+    border may lie too; all negative; ranges beyond the places."""
+    B, V = 12, 9001
+    x = spaced(3, B, V, centre, spread)
+    p = [0.3, 0.5, 0.7, 0.9, 0.99, 0.999, 1.0, 1.0, 1.0, 0.5, 0.8, 0.6]
+    k = [0, 0, 0, 0, 0, 0, 7, 900, 5000, 2999, 20, 4000]
+    check(x, t=[t] * B, k=k, p=p, m=[0.0] * 10 + [0.3, 0.01], u=uniform(4, B))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+def test_many_equal_logits_at_the_border(dtype):
+    """Logits that were bf16 before, of a large vocabulary: hundreds of elements in a step, at borders far down."""
+    x = spaced(5, 6, 131072, 0.0, 2.0).to(dtype)
+    x[:, 5] = 9.0
+    check(x, t=[0.9, 1.0, 1.3, 0.6, 1.0, 1.0], p=[0.99, 0.9, 0.5, 0.95, 1.0, 0.7], k=[0, 0, 0, 0, 5000, 60000], u=uniform(6, 6))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+def test_top_p_next_to_one_and_to_nothing(dtype):
+    x = logits(7, 8, 20011, dtype)
+    p = [0.9999, 0.99999, 1.0 - 2.0 ** -24, 0.9997, 1e-30, 2.0 ** -40, 1e-3, 0.99]
+    check(x, p=p, u=uniform(8, 8))
+    check(x, p=p, k=[17000] * 8, u=uniform(9, 8))
+
+
+def test_draws_do_not_depend_on_the_rows_beside():
+    """A row alone, and among many (other clusters, other shares): the same token and log."""
+    x = logits(9, 300, 4001)
+    u, t = uniform(10, 300), [0.3 + (b % 7) * 0.2 for b in range(300)]
+    ids, lp = call(x, t=t, p=[0.9] * 300, u=u)
+    for b in (0, 7, 151, 299):
+        one, l1 = call(x[b:b + 1].contiguous(), t=t[b:b + 1], p=[0.9], u=u[b:b + 1])
+        assert (one[0], l1[0]) == (ids[b], lp[b])

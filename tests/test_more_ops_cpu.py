@@ -20,7 +20,8 @@ def copy(src=None, dst=None, n=1, first=OK, to=OK, length=OK, err=None):
     dict(n=0), dict(n=-1), dict(n=1025), dict(first=None), dict(to=None), dict(first=OK + 2), dict(to=OK + 1), dict(length=OK + 3), dict(err=OK + 2),
     dict(src=cache(head_dim=64)), dict(src=cache(block=32)), dict(dst=cache(format=rv.KV8_E4M3)), dict(dst=cache(act_dtype=rv.F16)),
     dict(src=cache(n_kv_heads=4)), dict(src=cache(k_codes=None)), dict(dst=cache(v_tail=OK + 8)), dict(dst=cache(v_scale=2 * OK)),
-    dict(src=cache(max_seq=999)), dict(src=cache(max_seq=0)), dict(dst=cache(max_batch=0)),
+    dict(src=cache(max_seq=999)), dict(src=cache(max_batch=3)), dict(src=cache(max_seq=0)),
+    dict(src=cache(k_codes=3 * OK, v_codes=4 * OK, k_scale=5 * OK, v_scale=6 * OK, k_tail=7 * OK)), dict(dst=cache(max_batch=0)),
     dict(src=cache(max_seq=2 ** 28), dst=cache(max_seq=2 ** 28))])
 def test_copy_refusals(kw):
     refused(copy, **kw)

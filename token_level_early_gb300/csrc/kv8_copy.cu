@@ -254,9 +254,9 @@ extern "C" int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const in
   if (!d_from || !d_to) return op_fail(RV_EINVAL, "d_from or d_to: null pointer");
   if (int rc = check_index(d_from, d_to, d_err)) return rc;
   if (int rc = check_index(d_len, nullptr, nullptr)) return rc;
-  const bool same = src->k_codes == dst->k_codes;
-  if (same && (src->v_codes != dst->v_codes || src->k_scale != dst->k_scale || src->v_scale != dst->v_scale || src->k_tail != dst->k_tail ||
-               src->v_tail != dst->v_tail || src->max_seq != dst->max_seq))
+  const int alike = (src->k_codes == dst->k_codes) + (src->v_codes == dst->v_codes) + (src->k_scale == dst->k_scale) +
+                    (src->v_scale == dst->v_scale) + (src->k_tail == dst->k_tail) + (src->v_tail == dst->v_tail);
+  if (alike != 0 && (alike != 6 || src->max_seq != dst->max_seq || src->max_batch != dst->max_batch))
     return op_fail(RV_EINVAL, "src and dst share a part of their memory");
   if ((int64_t)(src->max_seq < dst->max_seq ? src->max_seq : dst->max_seq) * dst->head_dim > INT32_MAX - 8192)
     return op_fail(RV_EINVAL, "max_seq x head_dim of both above 2^31");
