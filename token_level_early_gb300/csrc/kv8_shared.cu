@@ -4,8 +4,10 @@
 // out = (sum over the prefix + sum over the own positions) of w v / sum of w:
 // three kernels leave states (reference m, sum l, weighted sum O) and join them.
 // The own positions are the cache attention's (kv8_attention.cuh), which here
-// leaves its rows' states.  For the prefix, the fan x T x (H / Hkv) query rows
-// that share a KV head of a prefix row are taken together.
+// leaves its rows' states; the prefix, whose fan x T x (H / Hkv) query rows of a KV
+// head are taken together, is kv8_shared.cuh's.  That one needs no result of the
+// first and begins while it runs (the first lets it at once; it waits for the
+// first at its end, so that the join, which waits for it, has both).
 #include "kv8_shared.cuh"
 
 namespace rv {

@@ -10,12 +10,27 @@
 // they take their scores' place.  O stays in tensor memory.
 //
 // A block per SM: 4 or 8 warps turn codes to fp16, one thread issues the
-// products, 8 warps in two streams do the softmax, so that one's products run under the
-// other's weights.  Up to 128 query rows, the streams take every other tile of
-// positions and are joined at the end; with more, each has its 128 rows.  With 32
-// or 64 rows at most, the rows are there four times or twice, each time for
-// another part of a tile's positions (the others' weights are zero): the products
-// would take as long with empty rows, and so all warps share the weights.
+// products, 8 warps in two streams do the softmax, so that one's products run
+// under the other's weights.  Up to 128 query rows, the streams take every other
+// tile of positions and are joined at the end; with more, each has its 128 rows.
+// With 32 or 64 rows at most, the rows are there four times or twice, each time
+// for another part of a tile's positions (the others' weights are zero): the
+// products would take as long with empty rows, and so all warps share the
+// weights (16 prompts of 8 rows 60 -> 52 us with the rest).
+//
+// What bounds it: the chain S, weights, O of a stream.  For 256 query rows behind
+// 32,768 positions of 8 KV heads of 128 (a piece of 13.5 tiles for each SM) a
+// tile takes some 4,800 cycles, 2 x 1,040 of them products back to back (which is
+// what they take alone); of a stream's 4,800, 2,300 are softmax (max 620, weights
+// 1,500: 276 cycles per 32 positions alone, 380 here) and the rest products and
+// hand-overs (a wait on an mbarrier takes 200 cycles, done or not).  Measured and
+// dropped: two warps a row quarter, each half of the positions (72 registers, no
+// faster: 81.8 against 80.9 us then); a warp for each stream's products, taking
+// turns or not (the streams fall in step: 82.1 and 79.3 against 73.4 us); one lane
+// that asks for its warp (95.5); the next scores under way during the weights
+// (spills); hints of time with the waits, naps between tries (no change).  The
+// beginning takes 6 us (codes, queries and instructions come from far), the
+// states' way out 4: 152 blocks leave 256 rows of 512 bytes each.
 #pragma once
 
 #include <type_traits>
@@ -26,7 +41,6 @@
 
 namespace rv {
 namespace kv8s {
-
 
 using kv8a::ex2;
 using kv8a::kLog2e;
@@ -698,10 +712,10 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
     }
   }
   pdl_trigger();
-  pdl_wait();  // the join, which waits for this kernel, needs the one before too
   tmem_fence_before();
   __syncthreads();
   if (warp == kSoftWarps + kCodeWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+  pdl_wait();  // the join, which waits for this kernel, needs the one before too
 }
 
 template <int FMT, int HD, bool LO>
