@@ -243,6 +243,22 @@ def test_long_prefixes_and_every_split():
             assert abs(float(lse[b, 0, h]) - rl) <= lse_tolerance(rl, D)
 
 
+def test_many_short_prefixes():
+    """More units than blocks, most of one tile (a stream has nothing of them), 80 rows each: the streams
+    leave a unit's state at different times.  Every row against the definition, and the same bits again."""
+    P, fan, T, H, Hkv, hd, act = 90, 5, 4, 8, 2, 64, 1
+    lens = [(100, 128, 1, 300, 0, 64, 128)[p % 7] for p in range(P)]
+    pre, pk, pv = filled(1, P, Hkv, hd, 32, 0, act, lens, 300)
+    pos = [b % 4 - 2 for b in range(P * fan)]
+    own, ok, ov = filled(3, P * fan, Hkv, hd, 16, 0, act, [max(p + T, 0) for p in pos], 16)
+    q = queries(5, P * fan, T, H, hd, act)
+    out, lse = call(pre, own, q, fan, 0.125, lens, pos)
+    check(pre, own, pk, pv, ok, ov, q, fan, 0.125, lens, pos, None, out, lse)
+    for _ in range(20):
+        again, l2 = call(pre, own, q, fan, 0.125, lens, pos)
+        assert torch.equal(again, out) and torch.equal(l2, lse)
+
+
 def test_captured_and_replayed_beside_another_stream():
     """One graph per workspace on two streams at once, with lengths and positions that change between replays."""
     P, fan, T, H, Hkv, hd, act = 2, 8, 1, 8, 2, 128, 1

@@ -159,11 +159,15 @@ struct Bars {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2];  // streams
   uint64_t exchange, drained;
 };
-// What the block's threads share beside the operands.  Rows by stream.
-struct Side {
-  Bars bar;
+// What the streams' warps tell each other of a part: rows by stream.
+struct Told {
   float m[2][128], l[2][128];
   int e[2][4];
+};
+// What the block's threads share beside the operands.
+struct Side {
+  Bars bar;
+  Told told[2];  // by turns: a stream without items in a part writes its own before the other is through with the part before
   int scratch[threads_of(64) + 2];
   uint32_t tmem;
   int dead;  // a wait ran out: everyone leaves
@@ -393,7 +397,7 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
     const uint32_t lanes = (uint32_t)quarter << 21;  // the warp's first lane, in an address
     const uint32_t my_s = at_s(s) + lanes, my_o = at_o(s) + lanes;
     const int grp = a.H / c.Hkv, nb = kTile >> lb;  // blocks of a tile: their K scales in lanes 0.., their V scales in lanes 8..
-    uint32_t items = 0, outs = 0, exchanges = 0;
+    uint32_t items = 0, outs = 0, exchanges = 0, turn = 0;
     bool ok = true;
     while (ok && walk.next(a, part)) {
       const bool two = part.rows > 128;
@@ -627,10 +631,12 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
       if (any) ok = wait(&bar.o_full[s], outs++ & 1);
       if (!ok) break;
       if (!any) m = -INFINITY;
+      Told &told = side.told[turn];
+      turn ^= 1;
       const float2 l2 = f2_split(f2_add(l[0], l[1]));
-      side.l[s][r] = l2.x + l2.y;
-      side.m[s][r] = m;
-      if (lane == 0) side.e[s][quarter] = max(e, -126);
+      told.l[s][r] = l2.x + l2.y;
+      told.m[s][r] = m;
+      if (lane == 0) told.e[s][quarter] = max(e, -126);
       tmem_fence_before();
       __syncwarp();
       if (lane == 0) bar_arrive(&bar.exchange);
@@ -642,9 +648,9 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
       auto power = [&](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
       // O in units of 2^40 and of m's reference: the stream's own rows, or half of the elements of both streams' rows
       const int other = two ? s : s ^ 1, rr = two ? 128 * s + r : i_row;
-      float mm = fmaxf(side.m[s][r], side.m[other][r]);
-      for (int k = 0; k < times; ++k) mm = fmaxf(mm, fmaxf(side.m[s][k * span + i_row], side.m[other][k * span + i_row]));
-      const float g0 = ex2(side.m[s][r] - mm) * power(side.e[s][quarter]), g1 = ex2(side.m[other][r] - mm) * power(side.e[other][quarter]);
+      float mm = fmaxf(told.m[s][r], told.m[other][r]);
+      for (int k = 0; k < times; ++k) mm = fmaxf(mm, fmaxf(told.m[s][k * span + i_row], told.m[other][k * span + i_row]));
+      const float g0 = ex2(told.m[s][r] - mm) * power(told.e[s][quarter]), g1 = ex2(told.m[other][r] - mm) * power(told.e[other][quarter]);
       const bool others = !two && (s == 1 || tiles > 1);
       const int c0 = two ? 0 : s * (HD / 2), c1 = two ? HD : c0 + HD / 2;
       // with copies: through the queries' place (a row HD / 2 numbers, 16-byte pieces by piece ^ (row mod 8)), and summed
@@ -685,8 +691,8 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
       if (live && copy == 0 && (two || s == 0)) {
         float sum = 0.f;
         for (int k = 0; k < times; ++k) {
-          sum = fmaf(side.l[s][k * span + i_row], ex2(side.m[s][k * span + i_row] - mm), sum);
-          if (!two) sum = fmaf(side.l[1][k * span + i_row], ex2(side.m[1][k * span + i_row] - mm), sum);
+          sum = fmaf(told.l[s][k * span + i_row], ex2(told.m[s][k * span + i_row] - mm), sum);
+          if (!two) sum = fmaf(told.l[1][k * span + i_row], ex2(told.m[1][k * span + i_row] - mm), sum);
         }
         *reinterpret_cast<float2 *>(ml + 2 * rr) = make_float2(mm, sum);
       }
