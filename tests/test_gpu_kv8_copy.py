@@ -94,6 +94,15 @@ def test_copy_long_rows():
     check(c, c, [(0, 2, 20011), (2, 0, 19999)])
 
 
+@pytest.mark.parametrize("n", [1, 3, 5, 48])
+def test_copy_rows_with_many_scales(n):
+    """Several items of scales a head, the last of them short, rows that change places."""
+    c = random_cache(8, n + 1, 1, 64, 20011 if n < 48 else 3011, 16)
+    rng = np.random.default_rng(n)
+    to = rng.permutation(n + 1)
+    check(c, c, [(i, int(to[i]), int(rng.integers(c.T // 2, c.T + 1))) for i in range(n)])
+
+
 def test_a_fork_is_continued_as_the_source_could_be():
     """Fork inside a block, append different tokens to each: both hold what they
     were given, the open block quantised anew from the tail."""

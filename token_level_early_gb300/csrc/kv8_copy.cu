@@ -10,17 +10,21 @@
 //
 // Memory bounds it.  Bulk copies do the moving (each thread issues those of its
 // pairs), two buffers keep an item's loads on their way while the one before it
-// is written.  Measured: 16 forks of 32,768 positions of 8 KV heads of 128 (1.15 GB)
-// in 193 us, 5.95 TB/s, 88% of a copy's rate; 48 ragged rows in a new order (123
-// MB) in 29 us, 62%: a short kernel, whose blocks begin with three dependent
-// loads and end with their last items' stores.
+// is written.  Scales begin on 4-byte boundaries only and go through registers:
+// all threads share the words of an item, 8 loads each on their way, and an item
+// has few of them (a thread a pair, as it was: 3 rows of up to 45,380 positions
+// with 709 scales a head 50 us instead of 18.6).  Measured: 16 forks of 32,768
+// positions of 8 KV heads of 128 (1.15 GB) in 185 us, 6.2 TB/s, 92% of a copy's
+// rate; 48 ragged rows in a new order (123 MB) in 24.4 us, 74%: a short kernel,
+// whose blocks begin with three dependent loads and end with their last items'
+// stores; 3 rows of up to 45,380 positions (108 MB, some of it still in L2) in 15.3 us.
 #include "async.cuh"
 #include "ops.cuh"
 
 namespace rv {
 namespace {
 
-constexpr int kThreads = 64, kMaxPairs = 1024;
+constexpr int kThreads = 128, kMaxPairs = 1024;
 constexpr uint32_t kFree = 0xffffffffu;
 
 struct CopyArgs {
@@ -29,6 +33,7 @@ struct CopyArgs {
   const int32_t *from, *to, *len;
   int32_t *err;
   int chunk;  // bytes of an item in each row, a multiple of 16
+  int words;  // log2 of the 32-bit words of a scale item in each row
   int table;  // slots of the hash tables, a power of two above n
 };
 
@@ -108,53 +113,68 @@ __global__ void __launch_bounds__(kThreads) k_copy(const __grid_constant__ CopyA
     if (pairs[i].to >= 0) pairs[i].lead = a.n - (int)(best[pairs[i].lead] & 0xfff);
   __syncthreads();
 
-  // ---- items: [codes | tail | scales], each for K and V and every head
+  // ---- items: [scales | tail | codes], each for K and V and every head (scales go
+  // through registers, which takes its time: not at the end)
   const int lb = __ffs(a.dst.block) - 1, log_hd = hd == 64 ? 6 : 7, heads = 2 * a.dst.Hkv;
   const int tail_bytes = 4 * a.dst.block * hd, scale_bytes = (((s_most >> log_hd) + a.dst.block - 1) >> lb) * 4;
   const int n_codes = (s_most + a.chunk - 1) / a.chunk, n_tail = (tail_bytes + a.chunk - 1) / a.chunk;
-  const int n_scale = (scale_bytes + a.chunk - 1) / a.chunk;
+  const int n_scale = (scale_bytes + (4 << a.words) - 1) / (4 << a.words);
   const int64_t end = (int64_t)heads * (n_codes + n_tail + n_scale);
 
   struct Item {
-    int kind, kv, h, off;  // 0 codes, 1 tail, 2 scales; byte offset in a head's range
+    int kind, kv, h, off;  // 0 scales, 1 tail, 2 codes; byte offset in a head's range
   };
   auto item = [&](int64_t i) {
     Item t;
-    const int64_t c = (int64_t)heads * n_codes, d = c + (int64_t)heads * n_tail;
+    const int64_t c = (int64_t)heads * n_scale, d = c + (int64_t)heads * n_tail;
     t.kind = i < c ? 0 : i < d ? 1 : 2;
-    const int per = t.kind == 0 ? n_codes : t.kind == 1 ? n_tail : n_scale;
+    const int per = t.kind == 0 ? n_scale : t.kind == 1 ? n_tail : n_codes;
     const int64_t j = i - (t.kind == 0 ? 0 : t.kind == 1 ? c : d), head = j / per;
     t.kv = (int)(head & 1);
     t.h = (int)(head >> 1);
-    t.off = (int)(j - head * per) * a.chunk;
+    t.off = (int)(j - head * per) * (t.kind ? a.chunk : 4 << a.words);
     return t;
   };
   // where a row's bytes of the item begin, and how many of them pair p copies
   auto place = [&](const Kv8 &c, const Item &t, int row) {
     const int64_t r = (int64_t)row * c.Hkv + t.h;
-    if (t.kind == 0) return c.codes[t.kv] + r * c.N * hd + t.off;
+    if (t.kind == 2) return c.codes[t.kv] + r * c.N * hd + t.off;
     if (t.kind == 1) return reinterpret_cast<uint8_t *>(c.tail[t.kv]) + r * tail_bytes + t.off;
     return reinterpret_cast<uint8_t *>(c.scale[t.kv] + r * (c.N >> lb)) + t.off;
   };
   auto bytes_of = [&](const Item &t, const Pair &p) {
-    const int all = t.kind == 0 ? p.bytes : t.kind == 1 ? tail_bytes : (((p.bytes >> log_hd) + a.dst.block - 1) >> lb) * 4;
-    return p.to < 0 ? 0 : min(max(all - t.off, 0), a.chunk);
+    const int all = t.kind == 2 ? p.bytes : t.kind == 1 ? tail_bytes : (((p.bytes >> log_hd) + a.dst.block - 1) >> lb) * 4;
+    return p.to < 0 ? 0 : min(max(all - t.off, 0), t.kind ? a.chunk : 4 << a.words);
   };
   auto load = [&](const Item &t, int buf) {
     unsigned char *to = sm + buf * buffer;
     uint32_t total = 0;
-    if (t.kind < 2)
+    if (t.kind)
       for (int i = tid; i < a.n; i += kThreads)
         if (pairs[i].lead == i) total += bytes_of(t, pairs[i]);
     bar_arrive_tx(&full[buf], total);
-    for (int i = tid; i < a.n; i += kThreads) {
-      const Pair p = pairs[i];
-      const int n = p.lead == i ? bytes_of(t, p) : 0;
-      if (n == 0) continue;
-      const uint8_t *from = place(a.src, t, p.from);
-      if (t.kind < 2) bulk_load(to + (size_t)i * a.chunk, from, n, &full[buf]);
-      else  // scales begin on 4-byte boundaries
-        for (int k = 0; k < n; k += 4) *reinterpret_cast<uint32_t *>(to + (size_t)i * a.chunk + k) = *reinterpret_cast<const uint32_t *>(from + k);
+    if (t.kind) {
+      for (int i = tid; i < a.n; i += kThreads) {
+        const Pair p = pairs[i];
+        const int n = p.lead == i ? bytes_of(t, p) : 0;
+        if (n) bulk_load(to + (size_t)i * a.chunk, place(a.src, t, p.from), n, &full[buf]);
+      }
+    } else {  // scales begin on 4-byte boundaries: all threads, with some loads each on their way
+      const int all = a.n << a.words, within = (1 << a.words) - 1;
+      for (int k0 = tid; k0 < all; k0 += 8 * kThreads) {
+        uint32_t v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int k = k0 + u * kThreads, i = k >> a.words, off = (k & within) * 4;
+          v[u] = 0;
+          if (k < all && pairs[i].lead == i && off < bytes_of(t, pairs[i])) v[u] = *reinterpret_cast<const uint32_t *>(place(a.src, t, pairs[i].from) + off);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int k = k0 + u * kThreads;
+          if (k < all) *reinterpret_cast<uint32_t *>(to + (size_t)(k >> a.words) * a.chunk + (k & within) * 4) = v[u];
+        }
+      }
     }
   };
 
@@ -180,15 +200,20 @@ __global__ void __launch_bounds__(kThreads) k_copy(const __grid_constant__ CopyA
       if (more) bar_wait(&full[buf ^ 1], ((k + 1) >> 1) & 1);
     }
     if (__syncthreads_or(!ok)) break;  // (also: every thread's scales are in place)
-    for (int i = tid; i < a.n; i += kThreads) {
-      const Pair p = pairs[i];
-      const int n = bytes_of(cur, p);
-      if (n == 0) continue;
-      uint8_t *to = place(a.dst, cur, p.to);
-      const unsigned char *from = sm + buf * buffer + (size_t)p.lead * a.chunk;
-      if (cur.kind < 2) bulk_store(to, from, n);
-      else
-        for (int j = 0; j < n; j += 4) *reinterpret_cast<uint32_t *>(to + j) = *reinterpret_cast<const uint32_t *>(from + j);
+    const unsigned char *from = sm + buf * buffer;
+    if (cur.kind) {
+      for (int i = tid; i < a.n; i += kThreads) {
+        const Pair p = pairs[i];
+        const int n = bytes_of(cur, p);
+        if (n) bulk_store(place(a.dst, cur, p.to), from + (size_t)p.lead * a.chunk, n);
+      }
+    } else {
+      for (int k = tid; k < a.n << a.words; k += kThreads) {
+        const int i = k >> a.words, off = (k - (i << a.words)) * 4;
+        const Pair p = pairs[i];
+        if (off < bytes_of(cur, p)) *reinterpret_cast<uint32_t *>(place(a.dst, cur, p.to) + off) = *reinterpret_cast<const uint32_t *>(from + (size_t)p.lead * a.chunk + off);
+      }
+      fence_async_smem();  // bulk copies take the buffer next
     }
     bulk_commit();
     if (!more) break;
@@ -211,11 +236,13 @@ size_t copy_smem(int n, int chunk) { return 2 * (size_t)n * chunk + (size_t)n * 
 
 // The bytes of an item in each row: as much as brings 8 to 16 KB with all pairs,
 // 512 bytes at least while two blocks of it find room in an SM, and so little
-// that the blocks have a few items each.  (16 forks of 32K positions, 48 rows in
-// a new order: 1 KB and 512 bytes 197.7 and 29.2 us with 128 threads, 193.2 and
-// 29.3 with 64, 204.8 and 30.0 with 256; 2 KB and 512 bytes 214.7; 1 KB and 256
-// bytes 196.7 and 42.7; 512 and 128 bytes 220.4 and 42.9; 4 blocks in an SM 197.7,
-// 3 250.5, 5 207.0.)
+// that the blocks have a few items each.  (Blocks of 128 threads, 4 in an SM, 512
+// bytes, 1, 2 and 4 KB: 16 forks of 32K positions 356, 185, 204, - us (2 in an SM
+// at 2 KB); 8 rows in a new order 150, 78, 56, 55; 5 forks of 19K - , 83, 48, 46; 3
+// rows in a new order - , 48, 27, 18.6.  48 rows in a new order, 256 and 512 bytes:
+// 42.7 and 29.3 before scales had all threads, 24.4 at 512 since.  Blocks of 64
+// threads: 183 us for the 16 forks, 26.1 for the 48 rows, 19.9 for the 3; of 256:
+// 210, 25.2, 21.1.)
 int kv8_copy_chunk(int n, int64_t row_bytes, int n_sm) {
   int chunk = 64;
   while (chunk < 8192 && (chunk < 512 ? copy_smem(n, 2 * chunk) <= 110000 : 2 * chunk * n <= 16384)) chunk *= 2;
@@ -225,13 +252,17 @@ int kv8_copy_chunk(int n, int64_t row_bytes, int n_sm) {
 
 cudaError_t launch_kv8_copy(const Kv8 &src, const Kv8 &dst, int n, const int32_t *from, const int32_t *to, const int32_t *len, int32_t *err,
                             int n_sm, cudaStream_t s, int pdl) {
-  CopyArgs a{src, dst, n, from, to, len, err, 0, table_slots(n)};
+  CopyArgs a{src, dst, n, from, to, len, err, 0, 4, table_slots(n)};
   const int64_t row = (int64_t)2 * dst.Hkv * (src.N < dst.N ? src.N : dst.N) * dst.hd;
   a.chunk = kv8_copy_chunk(n, row, n_sm);
+  while (4 << (a.words + 1) <= a.chunk && n << (a.words + 1) <= 1024) ++a.words;
   const size_t smem = copy_smem(n, a.chunk);
   cudaError_t e = cudaFuncSetAttribute(k_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  const int per_sm = smem > 100000 ? 1 : smem > 70000 ? 2 : smem > 52000 ? 3 : 4;
+  // (8 blocks in an SM instead of 4: one to four rows of 3 to 45K positions 18.6 -> 15.3, 17.7 -> 17.6, 6.5 -> 5.6 and
+  // 6.9 -> 6.1 us; rows written at more places: 8 rows in a new order 55.9 -> 59.4, 16 forks 185 -> 198)
+  const int room = smem > 100000 ? 1 : smem > 70000 ? 2 : smem > 52000 ? 3 : 4;
+  const int per_sm = n <= 4 ? (int)(200000 / smem < 8 ? 200000 / smem : 8) : room;
   const int64_t items = row / a.chunk + 6 * dst.Hkv + 2 * dst.Hkv * (4 * dst.block * dst.hd / a.chunk + 1), most = (int64_t)per_sm * n_sm;
   return launch_k(k_copy, dim3((unsigned)(items < most ? items : most)), dim3(kThreads), smem, s, pdl, a);
 }
