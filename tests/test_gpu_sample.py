@@ -204,3 +204,28 @@ def test_draws_do_not_depend_on_the_rows_beside():
     for b in (0, 7, 151, 299):
         one, l1 = call(x[b:b + 1].contiguous(), t=t[b:b + 1], p=[0.9], u=u[b:b + 1])
         assert (one[0], l1[0]) == (ids[b], lp[b])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_more_rows_than_multiprocessors(dtype):
+    """Many short rows take other blocks than few: the same definition."""
+    B, V = 170, 2001
+    r = np.random.default_rng(9)
+    x = logits(17, B, V, dtype)
+    x[::7, ::3] = -math.inf
+    check(x, t=[float(v) for v in r.choice([0.0, 0.5, 1.0], B)], k=[int(v) for v in r.choice([0, 3, 50], B)],
+          p=[float(v) for v in r.choice([0.2, 0.9, 1.0], B)], m=[float(v) for v in r.choice([0.0, 0.02], B)], u=[float(v) for v in r.random(B)])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("B,V", [(170, 5001), (160, 40001)])
+def test_rows_alone_and_together(B, V, dtype):
+    """However many rows there are (and so however a row's work is cut), its draw is the same."""
+    r = np.random.default_rng(V)
+    x = logits(V, B, V, dtype)
+    kw = dict(t=[float(v) for v in r.choice([0.5, 1.0], B)], k=[int(v) for v in r.choice([0, 3, 50], B)],
+              p=[float(v) for v in r.choice([0.2, 0.9, 1.0], B)], m=[float(v) for v in r.choice([0.0, 0.02], B)], u=[float(v) for v in r.random(B)])
+    ids, lp = call(x, **kw)
+    for n in (1, 20):
+        for b in range(0, B - n + 1, 13):
+            assert call(x[b:b + n], **{a: v[b:b + n] for a, v in kw.items()}) == (ids[b:b + n], lp[b:b + n]), b

@@ -25,13 +25,11 @@
 // the cluster's barriers, not memory.  64 rows of 128,256 fp32 with settings of
 // their own: 58 us (33 MB: 0.6 TB/s); of a block's 50,000 cycles, two in an SM,
 // loading takes 5,000, counts 9,000, bounds 13,000 in five barriers, exact weights
-// 5,500, the border 8,000, the draw 4,000.  256 rows of bf16 under top-p: 193 us;
-// counting 32,768 elements takes 30,000 of 86,000 cycles (14.7 a warp's 32 atomics,
-// banks at random; two copies of the counts: 198 us).  200 rows of 50,257 fp16 with
-// a temperature alone: 37 us, half of it weights.  One row of 32,000: 16 us, eight
-// blocks and nine barriers.  Blocks of 1024 threads with shares twice as long:
-// 168 us for the bf16 rows, but 43.6 instead of 37.3 for fp16 and 18.9 instead of
-// 16.2 for one row; of 256 threads: 250, 48.6 and 19.8.
+// 5,500, the border 8,000, the draw 4,000.  256 rows of bf16 under top-p: 169 us;
+// counting takes a third of it (14.7 cycles a warp's 32 atomics, banks at random;
+// two copies of the counts: 198 us instead of 195, with blocks of 512).  200 rows
+// of 50,257 fp16 with a temperature alone: 37 us, half of it weights.  One row of
+// 32,000: 16 us, eight blocks and nine barriers.
 #include <math.h>
 
 #include "ops.cuh"
@@ -39,7 +37,7 @@
 namespace rv {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kLimbs = 3, kLimbBits = 14;
+constexpr int kBins = 2048, kLimbs = 3, kLimbBits = 14;
 constexpr int kSteps = 4096, kList = 1024;  // steps of the first count; elements that are listed at most
 constexpr float kOctaves = 41.9f;          // below the largest: weights beyond are zero
 constexpr int kMaxVocab = 1 << 18, kMaxCluster = 8;
@@ -153,6 +151,7 @@ __device__ __noinline__ u64 weight_plain(float x, float top, float tau) {
   return z > -42.0 ? (u64)rint(exp2(z + 40.0)) : 0;  // (NaN: 0)
 }
 
+template <int NT>  // threads of a block
 struct alignas(16) Shared {  // the row's share follows, in 16-byte pieces
   uint32_t table[256];
   union {
@@ -163,8 +162,8 @@ struct alignas(16) Shared {  // the row's share follows, in 16-byte pieces
     };
   };
   uint32_t list[kList];
-  u64 add[kThreads];
-  u64 warp[4 * kWarps];
+  u64 add[NT];
+  u64 warp[4 * NT / 32];
   u64 total[2][32];  // of all blocks, 8 for each sum; two, used in turn
   u64 small;         // bf16: the weight of the small values, in the block that has their place
   u64 before[4];     // results that one thread finds
@@ -173,12 +172,14 @@ struct alignas(16) Shared {  // the row's share follows, in 16-byte pieces
   int listed, gathered;
 };
 static_assert(kLimbs * kBins <= 2 * kSteps, "select's bins fit");
-static_assert(sizeof(Shared) + 66032 <= 113 * 1024, "two blocks in an SM");
-static_assert(sizeof(Shared) % 16 == 0, "the row's share is aligned");
+static_assert(sizeof(Shared<512>) + 66032 <= 113 * 1024, "two blocks in an SM");
+static_assert(sizeof(Shared<1024>) + 132032 <= 227 * 1024, "one block in an SM");
+static_assert(sizeof(Shared<512>) % 16 == 0 && sizeof(Shared<1024>) % 16 == 0, "the row's share is aligned");
 
 // Sums, and places in them, over a block.
-template <typename T, int N>
-__device__ __forceinline__ void block_scan(Shared *sh, const T (&mine)[N], T (&before)[N], T (&all)[N]) {
+template <typename T, int N, int NT>
+__device__ __forceinline__ void block_scan(Shared<NT> *sh, const T (&mine)[N], T (&before)[N], T (&all)[N]) {
+  constexpr int W = NT / 32;
   static_assert(N <= 4 && sizeof(T) <= 8, "room for the warps' sums");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();
@@ -191,27 +192,27 @@ __device__ __forceinline__ void block_scan(Shared *sh, const T (&mine)[N], T (&b
       if (lane >= o) x += y;
     }
     before[n] = x - mine[n];
-    if (lane == 31) reinterpret_cast<T *>(&sh->warp[n * kWarps])[warp] = x;
+    if (lane == 31) reinterpret_cast<T *>(&sh->warp[n * W])[warp] = x;
   }
   __syncthreads();
 #pragma unroll
   for (int n = 0; n < N; ++n) {  // every warp adds the warps' sums up for itself
-    T x = lane < kWarps ? reinterpret_cast<T *>(&sh->warp[n * kWarps])[lane] : T(0);
+    T x = lane < W ? reinterpret_cast<T *>(&sh->warp[n * W])[lane] : T(0);
     const T own = x;
 #pragma unroll
-    for (int o = 1; o < kWarps; o <<= 1) {
+    for (int o = 1; o < W; o <<= 1) {
       const T y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     before[n] += __shfl_sync(0xffffffffu, x - own, warp);
-    all[n] = __shfl_sync(0xffffffffu, x, kWarps - 1);
+    all[n] = __shfl_sync(0xffffffffu, x, W - 1);
   }
 }
 
-template <int DT>
+template <int DT, int NT>
 struct Row {
   static constexpr int PER = DT == RV_F32 ? 1 : 2;  // elements of a word
-  Shared *sh;
+  Shared<NT> *sh;
   const uint32_t *data;  // this block's share, as 32-bit words
   int words, n_words;    // of a thread, of the block
   int shift;             // index of the share's first element (may be negative: before the row)
@@ -362,7 +363,7 @@ struct Row {
     for (int round = 0; round < 4; ++round) {  // 3 at most: 11 bits of a key each
       const int down = max(0, 32 - __clz(hi - lo) - 11);  // (hi - lo) >> down < kBins
       __syncthreads();
-      for (int i = threadIdx.x; i < L * kBins; i += kThreads) sh->hist[i] = 0;
+      for (int i = threadIdx.x; i < L * kBins; i += NT) sh->hist[i] = 0;
       __syncthreads();
       each([&](float x, int e) {
         const uint32_t k = key_of(x);
@@ -377,11 +378,11 @@ struct Row {
       });
       sync();
       // a block takes a run of the bins, a thread a run of those
-      const int per_block = kBins / ranks, per = max(1, per_block / kThreads), b0 = rank * per_block + threadIdx.x * per;
+      const int per_block = kBins / ranks, per = max(1, per_block / NT), b0 = rank * per_block + threadIdx.x * per;
       const bool live = threadIdx.x * per < per_block;
-      u64 sums[kBins / kThreads], mine = 0;
+      u64 sums[kBins / NT], mine = 0;
 #pragma unroll
-      for (int j = 0; j < kBins / kThreads; ++j) {
+      for (int j = 0; j < kBins / NT; ++j) {
         sums[j] = 0;
         if (j < per && live) {
           for (int k = 0; k < ranks; ++k)
@@ -397,7 +398,7 @@ struct Row {
       u64 before = base + scan(mine, all);
       if (round == 0 && (to > all || to == 0)) return false;
 #pragma unroll
-      for (int j = 0; j < kBins / kThreads; ++j) {
+      for (int j = 0; j < kBins / NT; ++j) {
         if (j < per && live && before < to && to <= before + sums[j]) {
           tell(1, (uint32_t)(b0 + j));
           tell(1, before);
@@ -501,7 +502,8 @@ __device__ __forceinline__ u64 goal_of(float p, u64 all) {
 // block: of those with bit 63 of the weight top-k keeps the first k (0: no
 // top-k); p < 1: with `before` ahead of all of them and `rest` behind those in
 // question in the weight that top-p takes its part of.
-__device__ __noinline__ u64 resolve(Shared *sh, int all, u64 k, float p, u64 before, u64 rest) {
+template <int NT>
+__device__ __noinline__ u64 resolve(Shared<NT> *sh, int all, u64 k, float p, u64 before, u64 rest) {
   constexpr u64 EDGE = 1ull << 63;
   const int tid = threadIdx.x;
   u64 cut = ~0ull;
@@ -536,7 +538,7 @@ __device__ __noinline__ u64 resolve(Shared *sh, int all, u64 k, float p, u64 bef
   // sorted (Batcher's bitonic network), then prefix sums
   int most = 256;
   while (most < all) most *= 2;
-  for (int i = all + tid; i < most; i += kThreads) {
+  for (int i = all + tid; i < most; i += NT) {
     sh->order[i] = ~0ull;
     sh->weight[i] = 0;
   }
@@ -616,13 +618,13 @@ struct Values {
 // count times its weight, so the border is a value, with so many of the elements
 // that have it, by index.  `sum` becomes the weight of this thread's elements
 // that stay.  False: the border lies among the small ones.
-template <int DT>
-__device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values values, u64 k, float p, float least, u64 &sum) {
-  Shared *sh = r.sh;
+template <int DT, int NT>
+__device__ __noinline__ bool by_values(Row<DT, NT> &r, Kept &kept, const Values values, u64 k, float p, float least, u64 &sum) {
+  Shared<NT> *sh = r.sh;
   const int tid = threadIdx.x;
   const float bottom = kept.cut.bottom;
-  constexpr int MOST = kSteps / kThreads;
-  const int per_block = kSteps / r.ranks, per = max(1, per_block / kThreads), q0 = r.rank * per_block + tid * per, run = tid * per < per_block ? per : 0;
+  constexpr int MOST = kSteps / NT;
+  const int per_block = kSteps / r.ranks, per = max(1, per_block / NT), q0 = r.rank * per_block + tid * per, run = tid * per < per_block ? per : 0;
   u64 small = 0;
   r.each_bits([&](uint16_t bits, int) {
     const uint32_t q = values.place(bits);
@@ -703,7 +705,7 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
   // ---- a weight for each place; elements at the border count in units of 2^52
   constexpr u64 TIE = 1ull << 52;
   const float border = edge < kSteps ? values.value((int)edge) : 0.f;
-  for (int q = tid; q < kSteps; q += kThreads) {
+  for (int q = tid; q < kSteps; q += NT) {
     const float v = values.value(q);
     sh->value[q] = q == values.mid || q > (int)edge || !(v >= least) ? 0 : q == (int)edge ? TIE : weight(v, kept.s, kept.table);
   }
@@ -746,15 +748,15 @@ __device__ __noinline__ bool by_values(Row<DT> &r, Kept &kept, const Values valu
   return true;
 }
 
-template <int DT>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2 pow2) {
+template <int DT, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2 pow2) {
   extern __shared__ __align__(16) unsigned char sm[];
-  Shared *sh = reinterpret_cast<Shared *>(sm);
-  uint4 *data = reinterpret_cast<uint4 *>(sm + sizeof(Shared));
+  Shared<NT> *sh = reinterpret_cast<Shared<NT> *>(sm);
+  uint4 *data = reinterpret_cast<uint4 *>(sm + sizeof(Shared<NT>));
   constexpr int SIZE = DT == RV_F32 ? 4 : 2, EPG = 16 / SIZE;
   const int tid = threadIdx.x, ranks = (int)cluster_size(), rank = (int)cluster_rank(), b = blockIdx.x / ranks;
-  for (int i = tid; i < 256; i += kThreads) sh->table[i] = pow2.t[i];
-  for (int i = tid; i < 2 * kSteps; i += kThreads) sh->hist[i] = 0;
+  for (int i = tid; i < 256; i += NT) sh->table[i] = pow2.t[i];
+  for (int i = tid; i < 2 * kSteps; i += NT) sh->hist[i] = 0;
   if (tid == 0) {
     sh->listed = sh->gathered = 0;
     sh->small = 0;
@@ -771,7 +773,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int lead = (int)(row - base) / SIZE, g0 = rank * a.granules, total = (lead + a.V + EPG - 1) / EPG;
   const int mine = max(0, min(a.granules, total - g0));
   float top = -INFINITY;
-  Row<DT> r{sh, reinterpret_cast<const uint32_t *>(data), a.words, mine * 4, g0 * EPG - lead, rank, ranks, 0};
+  Row<DT, NT> r{sh, reinterpret_cast<const uint32_t *>(data), a.words, mine * 4, g0 * EPG - lead, rank, ranks, 0};
   const float tau = a.temperature ? a.temperature[b] : 1.f, draw = a.u[b];
   const float p = a.top_p ? a.top_p[b] : 1.f, lowest = a.min_p ? a.min_p[b] : 0.f;
   const int k = a.top_k ? a.top_k[b] : 0;
@@ -780,18 +782,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < Row<DT>::PER; ++j) top = fmaxf(top, r.value(w[i], j));  // (fmaxf passes over NaN)
+      for (int j = 0; j < Row<DT, NT>::PER; ++j) top = fmaxf(top, r.value(w[i], j));  // (fmaxf passes over NaN)
   };
   auto whole = [&](int g) { return (g0 + g) * EPG - lead >= 0 && (g0 + g + 1) * EPG - lead <= a.V; };
   constexpr int FLY = 6;
-  for (int g = tid; g < mine; g += FLY * kThreads) {
+  for (int g = tid; g < mine; g += FLY * NT) {
     uint4 v[FLY];
 #pragma unroll
     for (int q = 0; q < FLY; ++q)
-      if (g + q * kThreads < mine && whole(g + q * kThreads)) v[q] = reinterpret_cast<const uint4 *>(base)[g0 + g + q * kThreads];
+      if (g + q * NT < mine && whole(g + q * NT)) v[q] = reinterpret_cast<const uint4 *>(base)[g0 + g + q * NT];
 #pragma unroll
     for (int q = 0; q < FLY; ++q) {
-      const int at = g + q * kThreads;
+      const int at = g + q * NT;
       if (at >= mine) continue;
       if (!whole(at)) {
         uint32_t w[4] = {};
@@ -811,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   top = warp_max(top);
   if ((tid & 31) == 0) sh->warp[tid >> 5] = __float_as_uint(top);
   __syncthreads();
-  top = warp_max((tid & 31) < kWarps ? __uint_as_float((uint32_t)sh->warp[tid & 31]) : -INFINITY);
+  top = warp_max((tid & 31) < NT / 32 ? __uint_as_float((uint32_t)sh->warp[tid & 31]) : -INFINITY);
   if (ranks > 1) {
     cluster_wait();
     if (tid < ranks)  // (the first scan uses the other one)
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
         kept.cut = Cut{bottom, 0xffffffffu, INT32_MAX};
         sum = 0;
         __syncthreads();
-        for (int i = tid; i < 2 * kSteps; i += kThreads) sh->hist[i] = 0;
+        for (int i = tid; i < 2 * kSteps; i += NT) sh->hist[i] = 0;
         if (tid < 8) sh->found[tid] = 0xffffffffu;
         __syncthreads();
       }
@@ -886,8 +888,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     // ---- a block takes a run of the steps, a thread a run of those.  Bounds of each step's weight, of the largest: with A =
     // ln 2 x a step in octaves, a place f of 256 weighs (1 - A f / 256 + [0, 2.6 10^-5]) 2^(-step); places are off by 0.007
     // of a step at most (5 10^-5 of the weight), whole numbers by half a unit of 2^-40, the sums below by 2^-18
-    const int per_block = kSteps / ranks, per = max(1, per_block / kThreads), q0 = rank * per_block + tid * per, run = tid * per < per_block ? per : 0;
-    constexpr int MOST = kSteps / kThreads;
+    const int per_block = kSteps / ranks, per = max(1, per_block / NT), q0 = rank * per_block + tid * per, run = tid * per < per_block ? per : 0;
+    constexpr int MOST = kSteps / NT;
     constexpr float OCT = kOctaves / (kSteps - 2), A = 0.693147181f * OCT;
     float n[MOST], low[MOST], high[MOST], mine[3] = {0.f, 0.f, 0.f}, at[3], sums[3];  // counts are below 2^24: exact
 #pragma unroll
@@ -1007,11 +1009,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       kept.cut.key = (uint32_t)(cut >> 32);
       kept.cut.last = (int)(uint32_t)cut - r.shift;
       // listed elements that stay belong to the threads whose elements they are
-      for (int i = tid; i < sh->listed; i += kThreads) {
+      for (int i = tid; i < sh->listed; i += NT) {
         const int e = (int)sh->list[i];
         const float x = r.at(e);
         const u64 w = x >= least ? kept(x, e) : 0;
-        if (w) atomicAdd(&sh->add[e / Row<DT>::PER / a.words], w);
+        if (w) atomicAdd(&sh->add[e / Row<DT, NT>::PER / a.words], w);
       }
       __syncthreads();
       sum += sh->add[tid];
@@ -1046,15 +1048,16 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   // (what a block reads or writes of another's shared memory lies before a barrier that the other one passes later)
 }
 
-template <int DT>
-cudaError_t launch_t(const SampleArgs &a, const Pow2 &t, int ranks, cudaStream_t s, int pdl) {
-  const size_t smem = sizeof(Shared) + (size_t)a.granules * 16;
-  auto fn = k_sample<DT>;
+template <int DT, int NT>
+cudaError_t launch_t(SampleArgs a, const Pow2 &t, int ranks, cudaStream_t s, int pdl) {
+  a.words = ((a.granules * 4 + NT - 1) / NT) | 1;
+  const size_t smem = sizeof(Shared<NT>) + (size_t)a.granules * 16;
+  auto fn = k_sample<DT, NT>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.B * ranks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(NT);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
@@ -1080,13 +1083,27 @@ const Pow2 &pow2_table() {
 
 }  // namespace
 
-// Blocks of a row's cluster: as many as leave room for two blocks in an SM's
-// shared memory, and more while the rows alone do not fill the GPU and a block
-// keeps 8 KB.
-int sample_cluster(int B, int64_t row_bytes, int n_sm) {
+// Threads of a block: 1024 and an SM for itself for bf16, whose 4096 values are
+// gone through three times whatever the row's length; 512 and two blocks in an SM
+// for the others, and where there are more short rows than SMs.  (512 / 1024, us,
+// the better cluster of each.  bf16 under top-p: one row of 1,000 16.3 / 14.3, of
+// 24,000 21.8 / 19.6, 100 of 8,000 23.1 / 19.6, 150 of 50,257 45.9 / 34.0, 70 of
+// 128,256 59.5 / 50.3, 256 of them 195 / 169; 300 of 8,000 29.9 / 36.9, 300 of
+// 24,000 46.7 / 50.0, 512 of 32,000 102 / 100.  fp32: one row of 32,000 16.5 / 19.1,
+// 64 of 128,256 58.0 / 59.3, 472 of 422 27.1 / 47.6; fp16: 148 of 10,487 20.9 /
+// 21.3, 200 of 50,257 37.6 / 43.9.)
+int sample_threads(int B, int vocab, bool bf16, int n_sm) { return bf16 && (B <= n_sm || vocab >= 32768) ? 1024 : 512; }
+
+// Blocks of a row's cluster: as many as its share of an SM's shared memory asks
+// for, and more while there is an SM for each and a thread keeps 16 bytes.
+// (1 / 2 / 4 / 8 blocks, us: 148 rows of 10,487 fp16 under top-p 20.9 / 27.9 /
+// 47.7 / 91, 100 of 20,000 bf16 32.1 / 33.8 / 46.8 / 71, 30 of 50,257 bf16 - /
+// 37.7 / 28.5 / 29.6, 64 of 32,000 fp32 - / 36.7 / 36.3 / 51.5, one of 32,000 - /
+// 26.2 / 19.2 / 16.7, 8 of 4,000 13.4 / 15.1 / 15.0 / 14.4.  With 512 threads.)
+int sample_cluster(int B, int64_t row_bytes, int n_sm, int threads) {
   int ranks = 1;
-  while (ranks < kMaxCluster && row_bytes > (int64_t)ranks * 66000) ranks *= 2;
-  while (ranks < kMaxCluster && (int64_t)B * ranks * 2 <= 2 * n_sm && row_bytes >= (int64_t)ranks * 16384) ranks *= 2;
+  while (ranks < kMaxCluster && row_bytes > (int64_t)ranks * (threads / 512) * 66000) ranks *= 2;
+  while (ranks < kMaxCluster && (int64_t)B * ranks * 2 <= n_sm && row_bytes >= (int64_t)ranks * (threads / 512) * 16384) ranks *= 2;
   return ranks;
 }
 
@@ -1115,17 +1132,18 @@ extern "C" int rv_sample(const void *d_logits, int dtype, int64_t stride, int B,
     if (int rc = check_device(names[i], words[i])) return rc;
   int n_sm = 0;
   if (int rc = sm_count(&n_sm)) return rc;
-  const int ranks = sample_cluster(B, (int64_t)vocab * size, n_sm);
+  const int threads = sample_threads(B, vocab, dtype == RV_BF16, n_sm);
+  const int ranks = sample_cluster(B, (int64_t)vocab * size, n_sm, threads);
   SampleArgs a{};
   a.x = d_logits; a.stride = stride; a.B = B; a.V = vocab;
   const int total = (vocab * size + 14) / 16 + 1;  // 16-byte pieces that a row can touch
   a.granules = (total + ranks - 1) / ranks;
-  a.words = ((a.granules * 4 + kThreads - 1) / kThreads) | 1;
   a.temperature = d_temperature; a.top_k = d_top_k; a.top_p = d_top_p; a.min_p = d_min_p; a.u = d_u;
   a.ids = d_ids; a.logprob = d_logprob;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const Pow2 &t = pow2_table();
-  return launched("rv_sample", dtype == RV_F32    ? launch_t<RV_F32>(a, t, ranks, s, 1)
-                               : dtype == RV_BF16 ? launch_t<RV_BF16>(a, t, ranks, s, 1)
-                                                  : launch_t<RV_F16>(a, t, ranks, s, 1));
+  return launched("rv_sample", dtype == RV_F32    ? launch_t<RV_F32, 512>(a, t, ranks, s, 1)
+                               : dtype == RV_F16  ? launch_t<RV_F16, 512>(a, t, ranks, s, 1)
+                               : threads == 512   ? launch_t<RV_BF16, 512>(a, t, ranks, s, 1)
+                                                  : launch_t<RV_BF16, 1024>(a, t, ranks, s, 1));
 }
