@@ -300,3 +300,41 @@ def test_workspace_of_the_largest_serves_the_smaller():
     with pytest.raises(rv.RVError):
         rv.kv8_attention_shared(pre.c, own.c, rv.heads(q), rv.heads(q), 12, 1, 6, 0.1, None, None, None, None, None,
                                 torch.zeros(64, dtype=torch.uint8).cuda().data_ptr(), 64)
+
+
+@pytest.mark.parametrize("long", [64, 40000])
+def test_both_caches_are_read_as_the_call_before_left_them(long):
+    """Appends to the prefix and to the own rows, each followed at once by the attention that reads
+    them, chained in a graph: the bits of the same calls one at a time.  `long`: room in the own
+    rows, which decides whether their part is one kernel or two."""
+    Hkv, hd, B, n, steps = 2, 128, 6, 1500, 8
+    pre, own = Cache(1, Hkv, hd, n, 64, 0, 1), Cache(B, Hkv, hd, long, 16, 0, 1)
+    ks, vs = ([data(10 * i + j, 1, n, Hkv, hd, 1) for i in range(steps)] for j in (1, 2))
+    ko, vo = ([data(10 * i + j, B, 5, Hkv, hd, 1) for i in range(steps)] for j in (3, 4))
+    qs = [queries(i, B, 1, 8, hd, 1) for i in range(steps)]
+    zero, pos = torch.zeros(B, dtype=torch.int32).cuda(), torch.full((B,), 4, dtype=torch.int32).cuda()
+    need = rv.kv8_attention_shared_workspace(pre.c, own.c, B, 1, B, 8)
+    work = torch.full((need,), 0xFF, dtype=torch.uint8).cuda()
+
+    def steps_of(outs, stream, wait):
+        for i in range(steps):
+            rv.kv8_append(own.c, rv.heads(ko[i]), rv.heads(vo[i]), B, 5, zero.data_ptr(), None, own.err.data_ptr(), stream)
+            rv.kv8_append(pre.c, rv.heads(ks[i]), rv.heads(vs[i]), 1, n, zero.data_ptr(), None, pre.err.data_ptr(), stream)
+            wait()
+            rv.kv8_attention_shared(pre.c, own.c, rv.heads(qs[i]), rv.heads(outs[i]), B, 1, B, 0.1, None, pos.data_ptr(), None, None, own.err.data_ptr(),
+                                    work.data_ptr(), need, stream)
+            wait()
+
+    want, got = [torch.zeros_like(q) for q in qs], [torch.zeros_like(q) for q in qs]
+    torch.cuda.synchronize()
+    steps_of(want, None, torch.cuda.synchronize)
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=stream):
+        steps_of(got, stream.cuda_stream, lambda: None)
+    for _ in range(30):
+        for x in got:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert int(pre.err) == 0 and int(own.err) == 0

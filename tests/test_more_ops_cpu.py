@@ -5,6 +5,7 @@ import math
 
 import pytest
 
+import test_ops_sources_cpu as sources
 import token_level_early_gb300 as rv
 from answers_util import draw
 from test_ops_cpu import OK, cache, heads, refused
@@ -93,3 +94,10 @@ def test_draw_closed_forms():
     assert draw([1.0, 1.0, 1.0, 1.0], 0.7, 0, 0.5, 0.0, 0.999)[0] == 1
     assert draw([-math.inf, math.nan], 1.0, 0, 1.0, 0.0, 0.5) == (-1, -math.inf)
     assert draw([0.0, math.inf, 3.0, math.inf], 1.0, 0, 1.0, 0.0, 0.6)[0] == 3
+
+
+# ------------------------------------------------------------------ sources
+
+@pytest.mark.parametrize("name", ["kv8_copy.cu", "kv8_shared.cuh", "kv8_shared.cu", "kv8_shared_e4m3.cu", "sample.cu"])
+def test_no_read_only_loads(name):
+    sources.test_no_read_only_loads_in_chained_kernels(name)

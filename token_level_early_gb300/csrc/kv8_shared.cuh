@@ -258,7 +258,9 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
   __syncthreads();
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, side.tmem, 0);
-  // (no wait for the kernel before: it reads other positions, and all that this one reads or overwrites was done before it began)
+  // No wait for the kernel before: it reads other positions, and all that this one reads or overwrites was done before it
+  // began, since every block of that one has waited for it.  Lines of before that may be in this SM are given up (0.4 us).
+  __threadfence();
   const Piece piece = cut_line<threads_of(HD)>(a, side.scratch);
   Walk walk{piece.begin, piece.end, piece.off, piece.p, piece.n};
   const Kv8 &c = a.c;
