@@ -230,6 +230,8 @@ int table_slots(int n) {
   while (t < 2 * n) t *= 2;
   return t;
 }
+// (the kernel's limit is the same for every call: calls of several threads may come between one's setting of it and its launch)
+constexpr int kMostSmem = 226 * 1024;
 size_t copy_smem(int n, int chunk) { return 2 * (size_t)n * chunk + (size_t)n * sizeof(Pair) + (size_t)table_slots(n) * 16; }
 
 }  // namespace
@@ -257,7 +259,7 @@ cudaError_t launch_kv8_copy(const Kv8 &src, const Kv8 &dst, int n, const int32_t
   a.chunk = kv8_copy_chunk(n, row, n_sm);
   while (4 << (a.words + 1) <= a.chunk && n << (a.words + 1) <= 1024) ++a.words;
   const size_t smem = copy_smem(n, a.chunk);
-  cudaError_t e = cudaFuncSetAttribute(k_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  cudaError_t e = cudaFuncSetAttribute(k_copy, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (e != cudaSuccess) return e;
   // (8 blocks in an SM instead of 4: one to four rows of 3 to 45K positions 18.6 -> 15.3, 17.7 -> 17.6, 6.5 -> 5.6 and
   // 6.9 -> 6.1 us; rows written at more places: 8 rows in a new order 55.9 -> 59.4, 16 forks 185 -> 198)
