@@ -31,6 +31,31 @@ def at_once(jobs, rounds):
     return raised
 
 
+@pytest.mark.parametrize("dtype,code", [(torch.float32, 2), (torch.bfloat16, 1), (torch.float16, 0)])
+def test_draws_of_different_vocabularies(dtype, code):
+    """Rows of other lengths take other amounts of shared memory: no call may take another's limit for its own."""
+    sides = []
+    for seed, V in enumerate((300, 24000, 120000, 9001)):
+        x = (torch.randn(2, V, generator=torch.Generator().manual_seed(seed)) * 3).to(dtype).cuda()
+        sides.append(dict(V=V, x=x, u=torch.tensor([0.3, 0.8]).cuda(), p=torch.full((2,), 0.9).cuda(), ids=torch.full((2,), -7, dtype=torch.int32).cuda(),
+                          s=torch.cuda.Stream()))
+
+    def call(d, stream):
+        rv.sample(d["x"].data_ptr(), code, d["V"], 2, d["V"], None, None, d["p"].data_ptr(), None, d["u"].data_ptr(), d["ids"].data_ptr(), None, stream)
+
+    torch.cuda.synchronize()
+    for d in sides:
+        call(d, None)
+    torch.cuda.synchronize()
+    want = [d["ids"].tolist() for d in sides]
+    for d in sides:
+        d["ids"].fill_(-7)
+    torch.cuda.synchronize()
+    raised = at_once([lambda i, d=d: call(d, d["s"].cuda_stream) for d in sides], 1500)
+    assert not raised, raised[0]
+    assert [d["ids"].tolist() for d in sides] == want
+
+
 def test_copies_of_different_numbers_of_pairs():
     sides = []
     for n in (1, 7, 40, 300):

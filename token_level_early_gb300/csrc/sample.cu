@@ -1053,7 +1053,8 @@ cudaError_t launch_t(SampleArgs a, const Pow2 &t, int ranks, cudaStream_t s, int
   a.words = ((a.granules * 4 + NT - 1) / NT) | 1;
   const size_t smem = sizeof(Shared<NT>) + (size_t)a.granules * 16;
   auto fn = k_sample<DT, NT>;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // (one limit for every call: calls of several threads may come between one's setting of it and its launch)
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.B * ranks);
