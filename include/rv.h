@@ -486,7 +486,8 @@ size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads
  * nearer end: a row or a length that is too large sets bit 6 (64) of *d_err (or
  * NULL: not reported).  src and dst agree in n_kv_heads, head_dim, block,
  * format and act_dtype; they are one cache (all six pointers, max_batch and
- * max_seq the same) or have no memory in common.  n is at most 1024. */
+ * max_seq the same) or have no memory in common (RV_EINVAL; two ranges of rows of
+ * the same arrays that do not meet are two caches).  n is at most 1024. */
 int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const int32_t *d_from, const int32_t *d_to, const int32_t *d_len,
                 int32_t *d_err, void *stream);
 

@@ -275,6 +275,33 @@ cudaError_t launch_kv8_copy(const Kv8 &src, const Kv8 &dst, int n, const int32_t
 
 using namespace rv;
 
+namespace {
+
+// The memory of a cache's six arrays; an end behind the last address is the last address.
+struct Spans {
+  uintptr_t from[6], to[6];
+};
+Spans spans_of(const rv_kv8 *c) {
+  const void *p[6] = {c->k_codes, c->v_codes, c->k_scale, c->v_scale, c->k_tail, c->v_tail};
+  const uint64_t rows = (uint64_t)c->max_batch * c->n_kv_heads, blocks = ((uint64_t)c->max_seq + c->block - 1) / c->block;
+  const uint64_t row[3] = {blocks * c->block * c->head_dim, blocks * 4, (uint64_t)4 * c->block * c->head_dim};  // codes, scales, tail
+  Spans s;
+  for (int i = 0; i < 6; ++i) {
+    s.from[i] = reinterpret_cast<uintptr_t>(p[i]);
+    s.to[i] = rows > (UINTPTR_MAX - s.from[i]) / row[i / 2] ? UINTPTR_MAX : s.from[i] + rows * row[i / 2];
+  }
+  return s;
+}
+bool share_memory(const rv_kv8 *a, const rv_kv8 *b) {
+  const Spans x = spans_of(a), y = spans_of(b);
+  for (int i = 0; i < 6; ++i)
+    for (int j = 0; j < 6; ++j)
+      if (x.from[i] < y.to[j] && y.from[j] < x.to[i]) return true;
+  return false;
+}
+
+}  // namespace
+
 extern "C" int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const int32_t *d_from, const int32_t *d_to, const int32_t *d_len,
                            int32_t *d_err, void *stream) {
   set_error_message("");
@@ -289,7 +316,8 @@ extern "C" int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const in
   if (int rc = check_index(d_len, nullptr, nullptr)) return rc;
   const int alike = (src->k_codes == dst->k_codes) + (src->v_codes == dst->v_codes) + (src->k_scale == dst->k_scale) +
                     (src->v_scale == dst->v_scale) + (src->k_tail == dst->k_tail) + (src->v_tail == dst->v_tail);
-  if (alike != 0 && (alike != 6 || src->max_seq != dst->max_seq || src->max_batch != dst->max_batch))
+  const bool one = alike == 6 && src->max_seq == dst->max_seq && src->max_batch == dst->max_batch;
+  if (!one && share_memory(src, dst))
     return op_fail(RV_EINVAL, "src and dst share a part of their memory");
   if ((int64_t)(src->max_seq < dst->max_seq ? src->max_seq : dst->max_seq) * dst->head_dim > INT32_MAX - 8192)
     return op_fail(RV_EINVAL, "max_seq x head_dim of both above 2^31");
