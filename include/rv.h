@@ -484,10 +484,13 @@ size_t rv_kv8_attention_workspace(const rv_kv8 *cache, int B, int T, int n_heads
  * with a negative row are passed over; rows at or beyond the cache's max_batch
  * are too, and lengths outside 0 .. the smaller max_seq are taken as the
  * nearer end: a row or a length that is too large sets bit 6 (64) of *d_err (or
- * NULL: not reported).  src and dst agree in n_kv_heads, head_dim, block,
- * format and act_dtype; they are one cache (all six pointers, max_batch and
- * max_seq the same) or have no memory in common (RV_EINVAL; two ranges of rows of
- * the same arrays that do not meet are two caches).  n is at most 1024. */
+ * NULL: not reported).  Every wait inside is bounded: one that runs out sets bit
+ * 4 (16), and the destinations, and in place the sources that are also
+ * destinations, are then not to be used: some are written and others not.  src
+ * and dst agree in n_kv_heads, head_dim, block, format and act_dtype; they are one
+ * cache (all six pointers, max_batch and max_seq the same) or have no memory in
+ * common (RV_EINVAL; two ranges of rows of the same arrays that do not meet are
+ * two caches).  n is at most 1024. */
 int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const int32_t *d_from, const int32_t *d_to, const int32_t *d_len,
                 int32_t *d_err, void *stream);
 
