@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(kWarps * 32, blocks_per_sm(HD, NT)) k_attn8(co
   __shared__ int s_see[ROWS];
   __shared__ int64_t s_tiles[kWarps], s_units[kWarps], s_off;
   __shared__ int s_row;
-  pdl_wait();
+  pdl_wait();  // (first of all: with `raw` the kernel behind rests on it, see ops.cuh)
   if (CL && a.raw) pdl_trigger();  // what comes next does not need this one's results before its end
   const Kv8 &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, tq = lane & 3;
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(256) k_attn8_join(const __grid_constant__ Kv8A
   __shared__ float s_x[8][HD], s_m[8], s_l[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = a.H / a.c.Hkv;
-  pdl_wait();
+  pdl_wait();  // (as in k_attn8)
   pdl_trigger();
   const Cut *cuts = static_cast<const Cut *>(a.work);
   const float *work = reinterpret_cast<const float *>(cuts + pieces);

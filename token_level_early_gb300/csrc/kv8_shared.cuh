@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(threads_of(HD), 1) k_prefix(const __grid_const
   tmem_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, side.tmem, 0);
   // No wait for the kernel before: it reads other positions, and all that this one reads or overwrites was done before it
-  // began, since every block of that one has waited for it.  Lines of before that may be in this SM are given up (0.4 us).
+  // began, since every block of that one has waited for it (the condition that this puts on it: ops.cuh).  Lines of before
+  // that may be in this SM are given up (0.4 us).
   __threadfence();
   const Piece piece = cut_line<threads_of(HD)>(a, side.scratch);
   Walk walk{piece.begin, piece.end, piece.off, piece.p, piece.n};

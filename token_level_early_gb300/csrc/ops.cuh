@@ -18,6 +18,16 @@ namespace rv {
 // is written during their lifetime, and none of them reads memory through the
 // read-only path (__ldg), which holds only for data that no one writes while
 // the kernel lives.
+//
+// One kernel waits only at its end: k_prefix (kv8_shared.cuh) reads queries,
+// lengths and codes, and writes its states, beside the kernel before it.  It may
+// because that one, the last that launch_kv8_attention launches with `raw` set
+// (k_attn8 or k_attn8_join), lets no successor start before each of its blocks
+// has waited: all that was in the stream before the call is done by then, the
+// readers of the workspace among them, and k_prefix touches nothing that the
+// call's own positions write.  So k_attn8 and k_attn8_join wait before anything
+// else and trigger only behind that, and nothing is launched between them and
+// k_prefix.
 
 // Records the message and returns the code.
 int op_fail(int code, const char *fmt, ...);
@@ -140,7 +150,9 @@ struct Kv8AttnArgs {
   float scale;
   const int32_t *pos, *count;
   float *lse;
-  float2 *raw;  // not NULL: out (RV_F32) receives weighted sums as they are, raw [B][T][H] their reference and sum, for a join
+  // not NULL: out (RV_F32) receives weighted sums as they are, raw [B][T][H] their reference and sum, for a join; the kernel
+  // behind begins without a wait (above)
+  float2 *raw;
   void *work;
   int cluster;  // blocks of a cluster (short contexts: a cluster per unit), or 0 (the cut line)
 };
