@@ -509,6 +509,14 @@ int rv_kv8_copy(const rv_kv8 *src, const rv_kv8 *dst, int n, const int32_t *d_fr
  * and held down to 2^-31 of the largest weight times the largest V scale of the
  * prefix.  Every wait inside is bounded: one that runs out sets bit 4 (16) of
  * *d_err (or NULL: not reported), and the outputs are then not to be used.
+ * In time it is ahead of rv_kv8_attention on rows that hold copies of the prefix
+ * where fan x prefix length is some 32,000 to 64,000 or more (one token, 8 KV
+ * heads of 128: 64 rows from 512 to 1,024 positions on, 32 from 1,024, 16 from
+ * 4,096, 8 from 8,192, 4 from 16,384 to 32,768), and behind it below: 4 rows behind 200
+ * positions take 12 us, copies of them 5.5.  For two rows it is behind up to
+ * 32,768 at least.  As there, the own part's plan follows the cache's max_seq, not
+ * the contents: 128 rows of up to 300 own positions (8 KV heads of 64) take 56 us
+ * with room for 1,024 and 73 with room for 4,096.
  * workspace: rv_kv8_attention_shared_workspace bytes, 16-byte aligned, no
  * contents needed or kept; calls that may run at the same time need one each. */
 int rv_kv8_attention_shared(const rv_kv8 *prefix, const rv_kv8 *cache, const rv_heads *q, const rv_heads *out, int B, int T, int fan,

@@ -15,7 +15,7 @@
 // has few of them (a thread a pair, as it was: 3 rows of up to 45,380 positions
 // with 709 scales a head 50 us instead of 18.6).  Measured: 16 forks of 32,768
 // positions of 8 KV heads of 128 (1.15 GB) in 185 us, 6.2 TB/s, 92% of a copy's
-// rate; 48 ragged rows in a new order (123 MB) in 24.4 us, 74%: a short kernel,
+// rate; 48 ragged rows in a new order (123 MB) in 24.4 to 24.9 us, 73%: a short kernel,
 // whose blocks begin with three dependent loads and end with their last items'
 // stores; 3 rows of up to 45,380 positions (108 MB, some of it still in L2) in 15.3 us.
 #include "async.cuh"
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) k_copy(const __grid_constant__ CopyA
   __syncthreads();
   for (int i = tid; i < a.table; i += kThreads) { keys[i] = kFree; value[i] = -1; }
   __syncthreads();
-  // longest first, the lower index among equals: (bytes, n - i) in one number (bytes < 2^38 / 2^6 in units of 64)
+  // longest first, the lower index among equals: bytes (below 2^31) x 2^12 + n - i (at most 1024)
   unsigned long long *best = reinterpret_cast<unsigned long long *>(value + a.table);
   for (int i = tid; i < a.table; i += kThreads) best[i] = 0;
   __syncthreads();

@@ -16,7 +16,7 @@
 // With 32 or 64 rows at most, the rows are there four times or twice, each time
 // for another part of a tile's positions (the others' weights are zero): the
 // products would take as long with empty rows, and so all warps share the
-// weights (16 prompts of 8 rows 60 -> 52 us with the rest).
+// weights (16 prompts of 8 rows 60 -> 52 us with the rest; 52 to 57 from run to run).
 //
 // What bounds it: the chain S, weights, O of a stream.  For 256 query rows behind
 // 32,768 positions of 8 KV heads of 128 (a piece of 13.5 tiles for each SM) a
@@ -149,7 +149,7 @@ constexpr int kSoftWarps = 8;
 // Warps that turn codes to fp16: 4 for K and V, or 4 for each where tiles are
 // short and follow one another sooner.  (4 / 8, with 128 / 96 registers a thread:
 // head_dim 128, 64 rows behind 32K positions 69.5 / 73.4 us; 64, 16 prompts of 8
-// rows 57.3 / 51.7.)
+// rows 57.3 / 51.7, each in one run: see above.)
 __host__ __device__ constexpr int code_warps(int hd) { return hd == 128 ? 4 : 8; }
 __host__ __device__ constexpr int threads_of(int hd) { return 32 * (kSoftWarps + code_warps(hd) + 1); }
 constexpr int kHalf = 16384;  // 128 rows of 64 fp16

@@ -23,13 +23,16 @@
 //
 // What bounds it: instructions (a weight is some 25), shared-memory atomics and
 // the cluster's barriers, not memory.  64 rows of 128,256 fp32 with settings of
-// their own: 58 us (33 MB: 0.6 TB/s); of a block's 50,000 cycles, two in an SM,
+// their own: 58 to 71 us by the settings (33 MB: 0.5 TB/s); of a block's 50,000 cycles, two in an SM,
 // loading takes 5,000, counts 9,000, bounds 13,000 in five barriers, exact weights
-// 5,500, the border 8,000, the draw 4,000.  256 rows of bf16 under top-p: 169 us;
+// 5,500, the border 8,000, the draw 4,000.  256 rows of bf16 under top-p: 169 to 188 us by the rows;
 // counting takes a third of it (14.7 cycles a warp's 32 atomics, banks at random;
 // two copies of the counts: 198 us instead of 195, with blocks of 512).  200 rows
-// of 50,257 fp16 with a temperature alone: 37 us, half of it weights.  One row of
-// 32,000: 16 us, eight blocks and nine barriers.
+// of 50,257 fp16 with a temperature alone: 37 us; of 80 warp instructions for 32
+// elements the weight (one for each, the draw adds those of a thread or so) is
+// some 25, the rest loading, the maximum, the loops and the cut's tests, which are
+// made although nothing is cut.  One row of 32,000: 16 to 18 us, eight blocks and
+// nine barriers.
 #include <math.h>
 
 #include "ops.cuh"
