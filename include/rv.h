@@ -538,8 +538,9 @@ size_t rv_kv8_attention_shared_workspace(const rv_kv8 *prefix, const rv_kv8 *cac
  *   d_top_p        of those, keep the ones before which less than top_p of
  *                  their weight lies in that order (the first at least); 1,
  *                  above or NaN: all
- *   d_min_p        keep those of at least min_p of the largest weight (1 at
- *                  most); 0, negative or NaN: all
+ *   d_min_p        keep those whose exp((x - max) / temperature), before it is
+ *                  rounded to a weight, is at least min_p (1 at most: the equals
+ *                  of the largest); 0, negative or NaN: all
  * The weight of logit x is w = round(2^40 exp((x - max) / temperature)), a whole
  * number: whatever weighs less than 2^-41 of the largest is never drawn, and the
  * result does not depend on the order of any sum.  d_ids[b] is the first token,
